@@ -1,0 +1,148 @@
+/*
+ * qta_layer.h -- C ABI of the layer operators next to the codec, for GB300
+ * (sm_103a): what a tensor-parallel layer computes before its output is
+ * compressed (linear layers with a fused epilogue, the gated feed-forward
+ * block) and after it was decompressed (residual add and norm), each with its
+ * backward pass.
+ *
+ * The conventions of qta.h hold: device pointers, caller-owned buffers, no
+ * allocation and no synchronisation inside the library, work enqueued on
+ * `stream`, errors returned before anything is enqueued, bounded waits whose
+ * expiry qta_device_error() reports.  In addition:
+ *  - A matrix is row-major with unit stride along a row and `ld` elements
+ *    between rows (qta_mat); rows may be slices of a larger buffer.
+ *  - Matrices that the matrix products read (x, w, wg, wu, dy, dh) need a
+ *    16-byte aligned base and, with more than one row, rows a multiple of 16
+ *    bytes apart, else QTA_ERR_ALIGNMENT; their lengths are free (elements
+ *    between a row's end and the next row are never used).  Every other
+ *    matrix and every vector needs the alignment of its element type only
+ *    (outputs that are not 16-byte aligned are stored element by element).
+ *  - `rows` (tokens) may be zero: forward calls do nothing, backward calls
+ *    write zeros to the weights' gradients.  Every other size is at least 1.
+ *  - An output may not share a byte with an input or another output
+ *    (QTA_ERR_INVALID_ARG), except that qta_linear's y may be its residual.
+ *  - Sums, statistics and activations are computed in FP32; a value is
+ *    rounded once to its output type (round to nearest even), except where a
+ *    call says that it keeps a 16-bit intermediate.  Infinities and NaN
+ *    propagate as FP32 arithmetic gives them, within their rows and columns.
+ *  - Every call is deterministic: bit-identical results run to run.
+ */
+#ifndef QTA_LAYER_H
+#define QTA_LAYER_H
+
+#include "qta.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    void* data;
+    int64_t ld; /* elements between rows; 0: the row length (contiguous) */
+} qta_mat;
+
+typedef enum { QTA_NORM_LAYER = 0, QTA_NORM_RMS = 1 } qta_norm_kind;
+
+/* Activations f(z): identity, max(z, 0), z sigmoid(z),
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), z/2 (1 + erf(z/sqrt 2)). */
+typedef enum {
+    QTA_ACT_NONE = 0,
+    QTA_ACT_RELU = 1,
+    QTA_ACT_SILU = 2,
+    QTA_ACT_GELU_TANH = 3,
+    QTA_ACT_GELU_ERF = 4
+} qta_act;
+
+typedef struct {
+    int64_t rows;    /* tokens */
+    int64_t cols;    /* channels, normalised together */
+    int32_t dtype;   /* qta_dtype of x, residual, y, sum, dy, dsum, dx */
+    int32_t w_dtype; /* qta_dtype of gamma and beta: dtype or QTA_FP32 */
+    int32_t kind;    /* qta_norm_kind */
+    float eps;       /* >= 0 and finite */
+} qta_norm_desc;
+
+typedef struct {
+    int64_t rows;       /* tokens */
+    int64_t n_out;      /* output channels: w is [n_out, n_in] */
+    int64_t n_in;       /* input channels */
+    int32_t dtype;      /* qta_dtype of x, w, dy, dx: QTA_BF16 or QTA_FP16 */
+    int32_t out_dtype;  /* qta_dtype of y and residual: dtype or QTA_FP32 */
+    int32_t bias_dtype; /* qta_dtype of bias: dtype or QTA_FP32 */
+    int32_t grad_dtype; /* qta_dtype of dw: dtype or QTA_FP32 */
+    int32_t act;        /* qta_act */
+} qta_linear_desc;
+
+typedef struct {
+    int64_t rows;       /* tokens */
+    int64_t hidden;     /* channels of x */
+    int64_t width;      /* channels of h: wg and wu are [width, hidden] */
+    int32_t dtype;      /* qta_dtype of x, wg, wu, h, dh, dx: QTA_BF16 or QTA_FP16 */
+    int32_t grad_dtype; /* qta_dtype of dwg and dwu: dtype or QTA_FP32 */
+    int32_t act;        /* qta_act */
+} qta_ffn_desc;
+
+/* qta_norm -- residual add and norm of every row.  s = x + residual (x alone
+ * where residual is NULL), formed in FP32 and not rounded before it is used;
+ * LAYER: mean = sum(s)/cols, var = sum((s - mean)^2)/cols, rstd =
+ * 1/sqrt(var + eps), y = (s - mean) rstd gamma + beta.  RMS: rstd =
+ * 1/sqrt(sum(s^2)/cols + eps), y = s rstd gamma (beta and mean must be NULL).
+ * x, residual, y, sum: [rows, cols] of dtype; sum (the new residual stream)
+ * may be NULL; gamma and beta [cols] of w_dtype, beta may be NULL; mean and
+ * rstd: f32 [rows] for the backward pass, may be NULL. */
+qta_status qta_norm(const qta_norm_desc* d, const qta_mat* x, const qta_mat* residual, const void* gamma,
+                    const void* beta, const qta_mat* y, const qta_mat* sum, float* mean, float* rstd,
+                    qta_stream_t stream);
+
+/* qta_norm_bwd -- gradients of qta_norm.  s is what was normalised (the
+ * forward's sum, or x), mean and rstd the forward's (mean NULL for RMS).
+ * With xh = (s - mean) rstd, t = dy gamma and <.> the mean over a row:
+ * dx = rstd (t - <t> - xh <t xh>) + dsum (RMS: without <t>), the gradient of
+ * x and of residual alike; dgamma = sum over rows of dy xh, dbeta = sum over
+ * rows of dy (f32 [cols] each).  dsum [rows, cols] is the gradient that
+ * reaches s from elsewhere, may be NULL; dbeta may be NULL.  ws: device,
+ * 16-byte aligned, qta_norm_bwd_workspace_bytes(d) bytes. */
+size_t qta_norm_bwd_workspace_bytes(const qta_norm_desc* d);
+qta_status qta_norm_bwd(const qta_norm_desc* d, const qta_mat* dy, const qta_mat* s, const void* gamma,
+                        const float* mean, const float* rstd, const qta_mat* dsum, const qta_mat* dx,
+                        float* dgamma, float* dbeta, void* ws, qta_stream_t stream);
+
+/* qta_linear -- y = f(x w^T + bias) + residual.  x [rows, n_in], w [n_out,
+ * n_in] of dtype, bias [n_out] of bias_dtype (NULL: none), residual and y
+ * [rows, n_out] of out_dtype (residual NULL: none; it may be y itself). */
+qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat* w, const void* bias,
+                      const qta_mat* residual, const qta_mat* y, qta_stream_t stream);
+
+/* qta_linear_bwd -- gradients of qta_linear (the residual's is dy itself).
+ * z = x w^T + bias is recomputed, dz = dy f'(z) kept in dtype for the
+ * products, dx = dz w, dw = dz^T x, dbias = sum over rows of dz before that
+ * rounding (f32 [n_out]).  f'(0) = 0 for ReLU.  dx [rows, n_in] of dtype, dw
+ * [n_out, n_in] of grad_dtype, dbias: each may be NULL (not computed).  dy
+ * [rows, n_out] of dtype.  ws: device, 16-byte aligned,
+ * qta_linear_bwd_workspace_bytes(d) bytes. */
+size_t qta_linear_bwd_workspace_bytes(const qta_linear_desc* d);
+qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta_mat* x, const qta_mat* w,
+                          const void* bias, const qta_mat* dx, const qta_mat* dw, float* dbias, void* ws,
+                          qta_stream_t stream);
+
+/* qta_gated_ffn -- h = f(x wg^T) * (x wu^T) in one kernel: both projections,
+ * the activation and the product.  x [rows, hidden], wg, wu [width, hidden],
+ * h [rows, width], all of dtype. */
+qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat* wg, const qta_mat* wu,
+                         const qta_mat* h, qta_stream_t stream);
+
+/* qta_gated_ffn_bwd -- gradients of qta_gated_ffn.  g = x wg^T and u = x wu^T
+ * are recomputed (no activation of the forward pass is needed), dg =
+ * dh u f'(g) and du = dh f(g) kept in dtype for the products, dx = dg wg +
+ * du wu, dwg = dg^T x, dwu = du^T x.  dx [rows, hidden] of dtype (may be
+ * NULL), dwg and dwu [width, hidden] of grad_dtype (both may be NULL).  ws:
+ * device, 16-byte aligned, qta_gated_ffn_bwd_workspace_bytes(d) bytes. */
+size_t qta_gated_ffn_bwd_workspace_bytes(const qta_ffn_desc* d);
+qta_status qta_gated_ffn_bwd(const qta_ffn_desc* d, const qta_mat* dh, const qta_mat* x, const qta_mat* wg,
+                             const qta_mat* wu, const qta_mat* dx, const qta_mat* dwg, const qta_mat* dwu,
+                             void* ws, qta_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* QTA_LAYER_H */

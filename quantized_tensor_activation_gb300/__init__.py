@@ -285,3 +285,19 @@ def taco_channel_amax(d: Desc, x, x_dtype: int, chan, stream=None) -> None:
 
 def taco_ash_update(chan, cols: int, stream=None) -> None:
     _check("taco_ash_update", lib().taco_ash_update(_ptr(chan), cols, _stream(stream)))
+
+
+# ---------------------------------------------------------------- layer operators
+# Loaded on first use: they take torch tensors, and this module works without torch.
+_LAYER = ("norm_desc", "linear_desc", "ffn_desc", "norm_bwd_workspace_bytes", "linear_bwd_workspace_bytes",
+          "gated_ffn_bwd_workspace_bytes", "alloc_workspace", "qta_norm", "qta_norm_bwd", "qta_linear",
+          "qta_linear_bwd", "qta_gated_ffn", "qta_gated_ffn_bwd")
+
+
+def __getattr__(name):
+    if name in _LAYER:
+        from . import layer
+        for n in _LAYER:
+            globals()[n] = getattr(layer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

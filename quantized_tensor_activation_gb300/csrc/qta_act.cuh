@@ -1,0 +1,93 @@
+// qta_act.cuh -- element types and activations of the layer operators.
+#pragma once
+
+#include "qta_device.cuh"
+
+namespace qta {
+
+// qta_dtype values (include/qta.h): 0 bf16, 1 fp16, 2 fp32.
+__host__ __device__ constexpr int dt_size(int dt) { return dt == 2 ? 4 : 2; }
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dt)
+{
+    if (dt == 2) return static_cast<const float*>(p)[i];
+    const unsigned short h = static_cast<const unsigned short*>(p)[i];
+    return dt == 0 ? __uint_as_float(static_cast<uint32_t>(h) << 16) : __half2float(__ushort_as_half(h));
+}
+
+__device__ __forceinline__ void store_elem(void* p, int64_t i, int dt, float v)
+{
+    if (dt == 2)
+        static_cast<float*>(p)[i] = v;
+    else if (dt == 0)
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Two 16-bit elements of one word as floats, and back (round to nearest even).
+__device__ __forceinline__ float2 unpack2(uint32_t w, int dt)
+{
+    return up2(dt == 0 ? bf16x2_to_pair(w) : f16x2_to_pair(w));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int dt)
+{
+    return dt == 0 ? pair_to_bf16x2(pk2(lo, hi)) : pair_to_f16x2(pk2(lo, hi));
+}
+
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU_TANH = 3, ACT_GELU_ERF = 4 };
+
+// 1 / (1 + e^-z) by the fast exponential and division: their errors (a few
+// ulp of FP32) are far below half an ulp of the 16-bit types the result is
+// rounded to.  e^-z = inf for z < -88.7 gives 0.
+__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// GELU's tanh form is z sigmoid(2 q) with q = sqrt(2/pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float gelu_tanh_2q(float z)
+{
+    return z * fmaf(0.0713548162726009f, z * z, 1.5957691216057308f);
+}
+
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    switch (act) {
+    case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case ACT_SILU: return z * sigmoid_fast(z);
+    case ACT_GELU_TANH: return z * sigmoid_fast(gelu_tanh_2q(z));
+    case ACT_GELU_ERF: return 0.5f * z * erfcf(-0.7071067811865476f * z);   // no cancellation for z << 0
+    default: return z;
+    }
+}
+
+// f(z) and f'(z).
+__device__ __forceinline__ void act_both(float z, int act, float& f, float& df)
+{
+    switch (act) {
+    case ACT_RELU:
+        f = z > 0.0f ? z : (z != z ? z : 0.0f);
+        df = z > 0.0f ? 1.0f : 0.0f;
+        return;
+    case ACT_SILU: {
+        const float p = sigmoid_fast(z);
+        f = z * p;
+        df = fmaf(f, 1.0f - p, p);
+        return;
+    }
+    case ACT_GELU_TANH: {
+        const float p = sigmoid_fast(gelu_tanh_2q(z));
+        f = z * p;
+        df = fmaf(f * (1.0f - p), fmaf(0.2140644488178027f, z * z, 1.5957691216057308f), p);
+        return;
+    }
+    case ACT_GELU_ERF: {
+        const float c = 0.5f * erfcf(-0.7071067811865476f * z);
+        f = z * c;
+        df = fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), c);
+        return;
+    }
+    default: f = z; df = 1.0f; return;
+    }
+}
+
+}  // namespace qta

@@ -1,0 +1,25 @@
+// qta_layer.cuh -- host-side launchers of the layer operators (internal).
+#pragma once
+
+#include "qta_gemm.cuh"
+#include "qta_launch.h"
+#include "qta_norm.cuh"
+
+namespace qta {
+
+cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_col_sum(const void* a, int64_t ld, int dt, int64_t rows, int64_t cols, int parts, float* part,
+                           cudaStream_t stream);
+cudaError_t launch_col_finish(const float* part, int64_t stride, int parts, int64_t cols, float* out,
+                              cudaStream_t stream);
+
+// The operand forms of the products: both contiguous along the contraction
+// (forward), B contiguous along its output index (dx = dz w), both (dw = dz^T x).
+enum GemmForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
+
+// Output columns of a tile of gemm_kernel for the given problem.
+int gemm_tile_cols(int form, int epi);
+cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
+
+}  // namespace qta

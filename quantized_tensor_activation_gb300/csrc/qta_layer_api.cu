@@ -1,0 +1,533 @@
+// qta_layer_api.cu -- the C ABI of the layer operators (include/qta_layer.h):
+// argument checks, tensor maps, and the launches of each call.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/qta_layer.h"
+#include "qta_layer.cuh"
+
+namespace qta {
+namespace {
+
+bool is16(int32_t dt) { return dt == QTA_BF16 || dt == QTA_FP16; }
+bool dtype_ok(int32_t dt) { return is16(dt) || dt == QTA_FP32; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// A checked matrix (or a vector: one row).
+struct View {
+    const void* p = nullptr;
+    int64_t rows = 0, cols = 0, ld = 0;
+    int es = 1;
+    void* w() const { return const_cast<void*>(p); }
+};
+
+// What a matrix has to satisfy.  `product`: TMA reads it.
+qta_status check_mat(const qta_mat* m, int64_t rows, int64_t cols, int32_t dt, bool product, View* v)
+{
+    if (!m || !m->data || m->ld < 0) return QTA_ERR_INVALID_ARG;
+    v->p = m->data;
+    v->rows = rows;
+    v->cols = cols;
+    v->es = dt_size(dt);
+    v->ld = m->ld ? m->ld : cols;
+    if (rows <= 1) v->ld = round_up(cols, 16);   // never stepped over
+    if (v->ld < cols) return QTA_ERR_INVALID_ARG;
+    if (v->ld > (int64_t(1) << 36) / v->es) return QTA_ERR_UNSUPPORTED;
+    const uintptr_t a = product ? 16 : v->es;
+    if (reinterpret_cast<uintptr_t>(v->p) % a) return QTA_ERR_ALIGNMENT;
+    if (product && (v->ld * v->es) % 16) return QTA_ERR_ALIGNMENT;
+    return QTA_OK;
+}
+
+qta_status check_vec(const void* p, int64_t n, int32_t dt, View* v)
+{
+    if (!p) return QTA_ERR_INVALID_ARG;
+    v->p = p;
+    v->rows = 1;
+    v->cols = v->ld = n;
+    v->es = dt_size(dt);
+    return reinterpret_cast<uintptr_t>(p) % v->es ? QTA_ERR_ALIGNMENT : QTA_OK;
+}
+
+View bytes_view(const void* p, size_t n)
+{
+    View v;
+    v.p = p;
+    v.rows = 1;
+    v.cols = v.ld = static_cast<int64_t>(n);
+    return v;
+}
+
+// Whether two matrices share a byte.  Two column slices of one buffer (the
+// same row distance) interleave without sharing any.
+bool share(const View& a, const View& b)
+{
+    if (!a.p || !b.p || !a.rows || !b.rows || !a.cols || !b.cols) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    const uintptr_t la = a.ld * a.es, lb = b.ld * b.es, wa = a.cols * a.es, wb = b.cols * b.es;
+    const uintptr_t xe = x + (a.rows - 1) * la + wa, ye = y + (b.rows - 1) * lb + wb;
+    if (x >= ye || y >= xe) return false;
+    if (a.rows > 1 && b.rows > 1 && la == lb) {
+        const uintptr_t off = y >= x ? (y - x) % la : (la - (x - y) % la) % la;   // b's first column within a's rows
+        if (off >= wa && off + wb <= la) return false;
+    }
+    return true;
+}
+
+// Every output against every input and every other output.
+struct Overlaps {
+    View in[8], out[6];
+    int n_in = 0, n_out = 0;
+    void input(const View& v) { in[n_in++] = v; }
+    void output(const View& v) { out[n_out++] = v; }
+    bool any() const
+    {
+        for (int i = 0; i < n_out; ++i) {
+            for (int j = 0; j < n_in; ++j)
+                if (share(out[i], in[j])) return true;
+            for (int j = i + 1; j < n_out; ++j)
+                if (share(out[i], out[j])) return true;
+        }
+        return false;
+    }
+};
+
+qta_status cuda_status(cudaError_t e) { return e == cudaSuccess ? QTA_OK : QTA_ERR_CUDA; }
+
+// Tensor map of a 16-bit matrix: boxes of 64 columns x `box_rows` rows.
+bool map_mat(CUtensorMap* m, const View& v, int box_rows)
+{
+    return encode_matrix16(m, v.p, v.cols, v.rows, v.ld, 64, box_rows);
+}
+
+cudaError_t zero_mat(const View& v, cudaStream_t s)
+{
+    if (!v.p) return cudaSuccess;
+    return cudaMemset2DAsync(v.w(), v.ld * v.es, 0, v.cols * v.es, v.rows, s);
+}
+
+// ---------------------------------------------------------------- norm
+qta_status check_norm_desc(const qta_norm_desc* d)
+{
+    if (!d) return QTA_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype) || (d->w_dtype != d->dtype && d->w_dtype != QTA_FP32)) return QTA_ERR_UNSUPPORTED;
+    if (d->kind != QTA_NORM_LAYER && d->kind != QTA_NORM_RMS) return QTA_ERR_UNSUPPORTED;
+    if (d->rows < 0 || d->cols < 1) return QTA_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.0f) || std::isinf(d->eps)) return QTA_ERR_INVALID_ARG;
+    if (d->rows >= (int64_t(1) << 31) || d->cols >= (int64_t(1) << 31)) return QTA_ERR_UNSUPPORTED;
+    return QTA_OK;
+}
+
+// Row partitions of a column sum: enough CTAs to fill the GPU, few enough
+// that the partial sums stay small.
+constexpr int64_t MAX_PARTS = 256;
+int col_parts(int64_t rows) { return static_cast<int>(rows < MAX_PARTS ? (rows > 0 ? rows : 1) : MAX_PARTS); }
+
+// ---------------------------------------------------------------- products
+qta_status check_sizes(int64_t rows, int64_t a, int64_t b)
+{
+    const int64_t lim = (int64_t(1) << 31) - 512;   // tile coordinates are 32-bit
+    if (rows < 0 || a < 1 || b < 1) return QTA_ERR_INVALID_ARG;
+    if (rows > lim || a > lim || b > lim) return QTA_ERR_UNSUPPORTED;
+    return QTA_OK;
+}
+
+qta_status check_linear_desc(const qta_linear_desc* d)
+{
+    if (!d) return QTA_ERR_INVALID_ARG;
+    if (!is16(d->dtype)) return QTA_ERR_UNSUPPORTED;
+    for (int32_t t : {d->out_dtype, d->bias_dtype, d->grad_dtype})
+        if (t != d->dtype && t != QTA_FP32) return QTA_ERR_UNSUPPORTED;
+    if (d->act < QTA_ACT_NONE || d->act > QTA_ACT_GELU_ERF) return QTA_ERR_UNSUPPORTED;
+    return check_sizes(d->rows, d->n_out, d->n_in);
+}
+
+qta_status check_ffn_desc(const qta_ffn_desc* d)
+{
+    if (!d) return QTA_ERR_INVALID_ARG;
+    if (!is16(d->dtype) || (d->grad_dtype != d->dtype && d->grad_dtype != QTA_FP32)) return QTA_ERR_UNSUPPORTED;
+    if (d->act < QTA_ACT_NONE || d->act > QTA_ACT_GELU_ERF) return QTA_ERR_UNSUPPORTED;
+    return check_sizes(d->rows, d->hidden, d->width);
+}
+
+// One launch: D[M, N] over contraction K of a[0] and b[0] (and of a[1], b[1]
+// where given: `groups` == 1 adds their product to the same D, 2 computes a
+// second D of a[1] and b[0]).  The epilogue fields of p are the caller's.
+qta_status run_gemm(int form, int epi, GemmParams& p, int32_t dt, const View* a0, const View* a1, const View* b0,
+                    const View* b1, int64_t M, int64_t N, int64_t K, int groups, cudaStream_t s)
+{
+    int sms = 0;
+    if (query_device(&sms, &p.err) != cudaSuccess) return QTA_ERR_CUDA;
+    const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
+    const int tile_n = gemm_tile_cols(form, epi);
+    const int a_rows = form == FORM_TN ? 64 : GEMM_BM;
+    const int b_rows = form == FORM_NT ? tile_n : 64;
+    if (!map_mat(&p.a[0], *a0, a_rows) || !map_mat(&p.b[0], *b0, b_rows)) return QTA_ERR_CUDA;
+    if (a1 && !map_mat(&p.a[1], *a1, a_rows)) return QTA_ERR_CUDA;
+    if (b1 && !map_mat(&p.b[1], *b1, b_rows)) return QTA_ERR_CUDA;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.nk0 = p.nk = static_cast<int>(ceil_div(K, GEMM_BK));
+    if (a1 && groups == 1 && !dual) p.nk *= 2;
+    p.tiles_m = static_cast<int>(ceil_div(M, GEMM_BM));
+    p.tiles_n = static_cast<int>(ceil_div(N, tile_n));
+    p.groups = groups;
+    if (static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups >= (int64_t(1) << 31)) return QTA_ERR_UNSUPPORTED;
+    p.idesc = idesc_f16(0, 0, dt == QTA_BF16, false, false);   // the launcher adds the tile
+    return cuda_status(launch_gemm(form, epi, p, sms, s));
+}
+
+GemmParams blank()
+{
+    GemmParams p;
+    std::memset(&p, 0, sizeof(p));
+    return p;
+}
+
+void set_out(GemmParams& p, int i, const View& v)
+{
+    p.out[i] = v.w();
+    p.ld_out[i] = v.ld;
+}
+
+// Workspace of the backward products: 16-bit intermediates of `width`
+// channels with rows on 16 bytes, then the partial column sums.
+size_t mid_bytes(int64_t rows, int64_t width) { return static_cast<size_t>(round_up(rows * round_up(width, 8) * 2, 256)); }
+View mid_view(void* ws, int i, int64_t rows, int64_t width)
+{
+    View v;
+    v.p = static_cast<uint8_t*>(ws) + i * mid_bytes(rows, width);
+    v.rows = rows;
+    v.cols = width;
+    v.ld = round_up(width, 8);
+    v.es = 2;
+    return v;
+}
+
+}  // namespace
+}  // namespace qta
+
+using namespace qta;
+
+extern "C" {
+
+qta_status qta_norm(const qta_norm_desc* d, const qta_mat* x, const qta_mat* residual, const void* gamma,
+                    const void* beta, const qta_mat* y, const qta_mat* sum, float* mean, float* rstd,
+                    qta_stream_t stream)
+{
+    qta_status st = check_norm_desc(d);
+    if (st != QTA_OK) return st;
+    if (d->kind == QTA_NORM_RMS && (beta || mean)) return QTA_ERR_INVALID_ARG;
+    if (d->rows == 0) return QTA_OK;
+    View vx, vr, vg, vb, vy, vs, vm, vd;
+    if ((st = check_mat(x, d->rows, d->cols, d->dtype, false, &vx)) != QTA_OK) return st;
+    if (residual && (st = check_mat(residual, d->rows, d->cols, d->dtype, false, &vr)) != QTA_OK) return st;
+    if ((st = check_vec(gamma, d->cols, d->w_dtype, &vg)) != QTA_OK) return st;
+    if (beta && (st = check_vec(beta, d->cols, d->w_dtype, &vb)) != QTA_OK) return st;
+    if ((st = check_mat(y, d->rows, d->cols, d->dtype, false, &vy)) != QTA_OK) return st;
+    if (sum && (st = check_mat(sum, d->rows, d->cols, d->dtype, false, &vs)) != QTA_OK) return st;
+    if (mean && (st = check_vec(mean, d->rows, QTA_FP32, &vm)) != QTA_OK) return st;
+    if (rstd && (st = check_vec(rstd, d->rows, QTA_FP32, &vd)) != QTA_OK) return st;
+    Overlaps o;
+    for (const View* v : {&vx, &vr, &vg, &vb}) o.input(*v);
+    for (const View* v : {&vy, &vs, &vm, &vd}) o.output(*v);
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    int sms = 0;
+    unsigned int* err = nullptr;
+    if (query_device(&sms, &err) != cudaSuccess) return QTA_ERR_CUDA;
+    NormParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = vx.p;
+    p.residual = vr.p;
+    p.gamma = gamma;
+    p.beta = beta;
+    p.y = vy.w();
+    p.sum = vs.w();
+    p.mean = mean;
+    p.rstd = rstd;
+    p.rows = d->rows;
+    p.cols = d->cols;
+    p.ld_x = vx.ld;
+    p.ld_r = vr.ld;
+    p.ld_y = vy.ld;
+    p.ld_s = vs.ld;
+    p.eps = d->eps;
+    p.dt = d->dtype;
+    p.w_dt = d->w_dtype;
+    p.rms = d->kind == QTA_NORM_RMS;
+    return cuda_status(launch_norm(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qta_norm_bwd_workspace_bytes(const qta_norm_desc* d)
+{
+    if (check_norm_desc(d) != QTA_OK) return 0;
+    return static_cast<size_t>(col_parts(d->rows)) * 2 * d->cols * sizeof(float);
+}
+
+qta_status qta_norm_bwd(const qta_norm_desc* d, const qta_mat* dy, const qta_mat* s, const void* gamma,
+                        const float* mean, const float* rstd, const qta_mat* dsum, const qta_mat* dx, float* dgamma,
+                        float* dbeta, void* ws, qta_stream_t stream)
+{
+    qta_status st = check_norm_desc(d);
+    if (st != QTA_OK) return st;
+    const bool rms = d->kind == QTA_NORM_RMS;
+    if (rms && (mean || dbeta)) return QTA_ERR_INVALID_ARG;
+    View vdy, vs, vg, vm, vr, vds, vdx, vdg, vdb;
+    if ((st = check_vec(dgamma, d->cols, QTA_FP32, &vdg)) != QTA_OK) return st;
+    if (dbeta && (st = check_vec(dbeta, d->cols, QTA_FP32, &vdb)) != QTA_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (d->rows == 0) {
+        if (share(vdg, vdb)) return QTA_ERR_INVALID_ARG;
+        cudaError_t e = zero_mat(vdg, cs);
+        return cuda_status(e == cudaSuccess ? zero_mat(vdb, cs) : e);
+    }
+    if ((st = check_mat(dy, d->rows, d->cols, d->dtype, false, &vdy)) != QTA_OK) return st;
+    if ((st = check_mat(s, d->rows, d->cols, d->dtype, false, &vs)) != QTA_OK) return st;
+    if ((st = check_vec(gamma, d->cols, d->w_dtype, &vg)) != QTA_OK) return st;
+    if (!rms && (st = check_vec(mean, d->rows, QTA_FP32, &vm)) != QTA_OK) return st;
+    if ((st = check_vec(rstd, d->rows, QTA_FP32, &vr)) != QTA_OK) return st;
+    if (dsum && (st = check_mat(dsum, d->rows, d->cols, d->dtype, false, &vds)) != QTA_OK) return st;
+    if ((st = check_mat(dx, d->rows, d->cols, d->dtype, false, &vdx)) != QTA_OK) return st;
+    if (!ws) return QTA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return QTA_ERR_ALIGNMENT;
+    Overlaps o;
+    for (const View* v : {&vdy, &vs, &vg, &vm, &vr, &vds}) o.input(*v);
+    for (const View* v : {&vdx, &vdg, &vdb}) o.output(*v);
+    o.output(bytes_view(ws, qta_norm_bwd_workspace_bytes(d)));
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    int sms = 0;
+    unsigned int* err = nullptr;
+    if (query_device(&sms, &err) != cudaSuccess) return QTA_ERR_CUDA;
+    NormBwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.dy = vdy.p;
+    p.s = vs.p;
+    p.gamma = gamma;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dsum = vds.p;
+    p.dx = vdx.w();
+    p.part = static_cast<float*>(ws);
+    p.dgamma = dgamma;
+    p.dbeta = dbeta;
+    p.rows = d->rows;
+    p.cols = d->cols;
+    p.ld_dy = vdy.ld;
+    p.ld_s = vs.ld;
+    p.ld_ds = vds.ld;
+    p.ld_dx = vdx.ld;
+    p.parts = col_parts(d->rows);
+    p.dt = d->dtype;
+    p.w_dt = d->w_dtype;
+    p.rms = rms;
+    return cuda_status(launch_norm_bwd(p, sms, cs));
+}
+
+qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat* w, const void* bias,
+                      const qta_mat* residual, const qta_mat* y, qta_stream_t stream)
+{
+    qta_status st = check_linear_desc(d);
+    if (st != QTA_OK) return st;
+    if (d->rows == 0) return QTA_OK;
+    View vx, vw, vb, vr, vy;
+    if ((st = check_mat(x, d->rows, d->n_in, d->dtype, true, &vx)) != QTA_OK) return st;
+    if ((st = check_mat(w, d->n_out, d->n_in, d->dtype, true, &vw)) != QTA_OK) return st;
+    if (bias && (st = check_vec(bias, d->n_out, d->bias_dtype, &vb)) != QTA_OK) return st;
+    if (residual && (st = check_mat(residual, d->rows, d->n_out, d->out_dtype, false, &vr)) != QTA_OK) return st;
+    if ((st = check_mat(y, d->rows, d->n_out, d->out_dtype, false, &vy)) != QTA_OK) return st;
+    Overlaps o;
+    for (const View* v : {&vx, &vw, &vb}) o.input(*v);
+    if (vr.p != vy.p || vr.ld != vy.ld) o.input(vr);   // y may be the residual itself
+    o.output(vy);
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    GemmParams p = blank();
+    p.act = d->act;
+    p.bias = bias;
+    p.bias_dt = d->bias_dtype;
+    p.aux = vr.p;
+    p.ld_aux = vr.ld;
+    p.aux_dt = p.out_dt = d->out_dtype;
+    set_out(p, 0, vy);
+    return run_gemm(FORM_NT, EPI_LINEAR, p, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Row partitions of dbias: one per 128-row tile where the epilogue sums dz,
+// else those of the column sum of dy.
+static int64_t bias_parts(const qta_linear_desc* d)
+{
+    return d->act == QTA_ACT_NONE ? col_parts(d->rows) : ceil_div(d->rows, GEMM_BM);
+}
+
+size_t qta_linear_bwd_workspace_bytes(const qta_linear_desc* d)
+{
+    if (check_linear_desc(d) != QTA_OK) return 0;
+    const size_t mid = d->act == QTA_ACT_NONE ? 0 : mid_bytes(d->rows, d->n_out);
+    return mid + static_cast<size_t>(bias_parts(d)) * d->n_out * sizeof(float);
+}
+
+qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta_mat* x, const qta_mat* w,
+                          const void* bias, const qta_mat* dx, const qta_mat* dw, float* dbias, void* ws,
+                          qta_stream_t stream)
+{
+    qta_status st = check_linear_desc(d);
+    if (st != QTA_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    View vdy, vx, vw, vb, vdx, vdw, vdb;
+    if (dw && (st = check_mat(dw, d->n_out, d->n_in, d->grad_dtype, false, &vdw)) != QTA_OK) return st;
+    if (dbias && (st = check_vec(dbias, d->n_out, QTA_FP32, &vdb)) != QTA_OK) return st;
+    if (d->rows == 0) {
+        if (share(vdw, vdb)) return QTA_ERR_INVALID_ARG;
+        cudaError_t e = zero_mat(vdw, cs);
+        return cuda_status(e == cudaSuccess ? zero_mat(vdb, cs) : e);
+    }
+    if ((st = check_mat(dy, d->rows, d->n_out, d->dtype, true, &vdy)) != QTA_OK) return st;
+    if ((st = check_mat(x, d->rows, d->n_in, d->dtype, true, &vx)) != QTA_OK) return st;
+    if ((st = check_mat(w, d->n_out, d->n_in, d->dtype, true, &vw)) != QTA_OK) return st;
+    if (bias && (st = check_vec(bias, d->n_out, d->bias_dtype, &vb)) != QTA_OK) return st;
+    if (dx && (st = check_mat(dx, d->rows, d->n_in, d->dtype, false, &vdx)) != QTA_OK) return st;
+    if (!ws) return QTA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return QTA_ERR_ALIGNMENT;
+    Overlaps o;
+    for (const View* v : {&vdy, &vx, &vw, &vb}) o.input(*v);
+    for (const View* v : {&vdx, &vdw, &vdb}) o.output(*v);
+    o.output(bytes_view(ws, qta_linear_bwd_workspace_bytes(d)));
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    const bool act = d->act != QTA_ACT_NONE;
+    View dz = vdy;
+    float* part = static_cast<float*>(ws);
+    if (act) {
+        dz = mid_view(ws, 0, d->rows, d->n_out);
+        part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + mid_bytes(d->rows, d->n_out));
+        GemmParams p = blank();
+        p.act = d->act;
+        p.bias = bias;
+        p.bias_dt = d->bias_dtype;
+        p.aux = vdy.p;
+        p.ld_aux = vdy.ld;
+        p.aux_dt = p.out_dt = d->dtype;
+        p.colsum = dbias ? part : nullptr;
+        set_out(p, 0, dz);
+        st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+                      cs);
+        if (st != QTA_OK) return st;
+    }
+    if (dbias) {
+        const int parts = static_cast<int>(bias_parts(d));
+        cudaError_t e = cudaSuccess;
+        if (!act) e = launch_col_sum(vdy.p, vdy.ld, d->dtype, d->rows, d->n_out, parts, part, cs);
+        if (e == cudaSuccess) e = launch_col_finish(part, d->n_out, parts, d->n_out, dbias, cs);
+        if (e != cudaSuccess) return QTA_ERR_CUDA;
+    }
+    if (dx) {
+        GemmParams p = blank();
+        p.out_dt = d->dtype;
+        set_out(p, 0, vdx);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1, cs);
+        if (st != QTA_OK) return st;
+    }
+    if (dw) {
+        GemmParams p = blank();
+        p.out_dt = d->grad_dtype;
+        set_out(p, 0, vdw);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1, cs);
+        if (st != QTA_OK) return st;
+    }
+    return QTA_OK;
+}
+
+qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat* wg, const qta_mat* wu,
+                         const qta_mat* h, qta_stream_t stream)
+{
+    qta_status st = check_ffn_desc(d);
+    if (st != QTA_OK) return st;
+    if (d->rows == 0) return QTA_OK;
+    View vx, vg, vu, vh;
+    if ((st = check_mat(x, d->rows, d->hidden, d->dtype, true, &vx)) != QTA_OK) return st;
+    if ((st = check_mat(wg, d->width, d->hidden, d->dtype, true, &vg)) != QTA_OK) return st;
+    if ((st = check_mat(wu, d->width, d->hidden, d->dtype, true, &vu)) != QTA_OK) return st;
+    if ((st = check_mat(h, d->rows, d->width, d->dtype, false, &vh)) != QTA_OK) return st;
+    Overlaps o;
+    for (const View* v : {&vx, &vg, &vu}) o.input(*v);
+    o.output(vh);
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    GemmParams p = blank();
+    p.act = d->act;
+    p.out_dt = d->dtype;
+    set_out(p, 0, vh);
+    return run_gemm(FORM_NT, EPI_GATED, p, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t qta_gated_ffn_bwd_workspace_bytes(const qta_ffn_desc* d)
+{
+    if (check_ffn_desc(d) != QTA_OK) return 0;
+    return 2 * mid_bytes(d->rows, d->width);
+}
+
+qta_status qta_gated_ffn_bwd(const qta_ffn_desc* d, const qta_mat* dh, const qta_mat* x, const qta_mat* wg,
+                             const qta_mat* wu, const qta_mat* dx, const qta_mat* dwg, const qta_mat* dwu, void* ws,
+                             qta_stream_t stream)
+{
+    qta_status st = check_ffn_desc(d);
+    if (st != QTA_OK) return st;
+    if (!dwg != !dwu) return QTA_ERR_INVALID_ARG;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    View vdh, vx, vg, vu, vdx, vdg, vdu;
+    if (dwg && (st = check_mat(dwg, d->width, d->hidden, d->grad_dtype, false, &vdg)) != QTA_OK) return st;
+    if (dwu && (st = check_mat(dwu, d->width, d->hidden, d->grad_dtype, false, &vdu)) != QTA_OK) return st;
+    if (d->rows == 0) {
+        if (share(vdg, vdu)) return QTA_ERR_INVALID_ARG;
+        cudaError_t e = zero_mat(vdg, cs);
+        return cuda_status(e == cudaSuccess ? zero_mat(vdu, cs) : e);
+    }
+    if ((st = check_mat(dh, d->rows, d->width, d->dtype, true, &vdh)) != QTA_OK) return st;
+    if ((st = check_mat(x, d->rows, d->hidden, d->dtype, true, &vx)) != QTA_OK) return st;
+    if ((st = check_mat(wg, d->width, d->hidden, d->dtype, true, &vg)) != QTA_OK) return st;
+    if ((st = check_mat(wu, d->width, d->hidden, d->dtype, true, &vu)) != QTA_OK) return st;
+    if (dx && (st = check_mat(dx, d->rows, d->hidden, d->dtype, false, &vdx)) != QTA_OK) return st;
+    if (!ws) return QTA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return QTA_ERR_ALIGNMENT;
+    Overlaps o;
+    for (const View* v : {&vdh, &vx, &vg, &vu}) o.input(*v);
+    for (const View* v : {&vdx, &vdg, &vdu}) o.output(*v);
+    o.output(bytes_view(ws, qta_gated_ffn_bwd_workspace_bytes(d)));
+    if (o.any()) return QTA_ERR_INVALID_ARG;
+
+    const View mg = mid_view(ws, 0, d->rows, d->width), mu = mid_view(ws, 1, d->rows, d->width);
+    {
+        GemmParams p = blank();
+        p.act = d->act;
+        p.aux = vdh.p;
+        p.ld_aux = vdh.ld;
+        p.aux_dt = p.out_dt = d->dtype;
+        set_out(p, 0, mg);
+        set_out(p, 1, mu);
+        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1, cs);
+        if (st != QTA_OK) return st;
+    }
+    if (dx) {
+        GemmParams p = blank();
+        p.out_dt = d->dtype;
+        set_out(p, 0, vdx);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1, cs);
+        if (st != QTA_OK) return st;
+    }
+    if (dwg) {
+        GemmParams p = blank();
+        p.out_dt = d->grad_dtype;
+        set_out(p, 0, vdg);
+        set_out(p, 1, vdu);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2, cs);
+        if (st != QTA_OK) return st;
+    }
+    return QTA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,88 @@
+// qta_tc.cuh -- 5th-generation tensor core building blocks (sm_103a): TMEM,
+// tcgen05.mma and its shared-memory descriptors.
+#pragma once
+
+#include "qta_device.cuh"
+
+namespace qta {
+
+// Instruction descriptor of tcgen05.mma.kind::f16: FP32 accumulator, A and B
+// both fp16 (0) or both bf16 (1), each K-major (contraction contiguous) or
+// MN-major (output index contiguous).
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool bf16, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled operand (the layout a TMA
+// box of 64 16-bit elements x rows writes; tiles start on 1024 bytes).
+//  K-major:  a row holds 64 contraction elements of one output index; groups
+//            of 8 rows are 1024 bytes apart (stride offset); 16 further
+//            contraction elements are 32 bytes further.
+//  MN-major: a row holds 64 output indices of one contraction element; groups
+//            of 8 contraction rows are 1024 bytes apart (stride offset), the
+//            next 64 output indices one box of 64 rows, 8192 bytes, further
+//            (leading offset); 16 further contraction rows are 2048 bytes further.
+constexpr uint32_t BOX_BYTES = 64 * 128;
+
+template <bool MN>
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
+{
+    const uint64_t lead = MN ? (BOX_BYTES >> 4) : 1u;
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (lead << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+template <bool MN>
+constexpr uint32_t K16_STEP = MN ? (2048u >> 4) : (32u >> 4);   // descriptor step of 16 contraction elements
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// The mbarrier completes when every tcgen05.mma this thread has issued is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 32 lanes (rows) x 32 columns of FP32 accumulators: column j in v[j].
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32])
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+}  // namespace qta

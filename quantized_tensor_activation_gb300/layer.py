@@ -1,0 +1,213 @@
+"""Layer operators next to the codec: residual add + norm, linear layers with a
+fused epilogue and the gated feed-forward block, each with its backward pass.
+
+The calls carry the names of the C ABI (``include/qta_layer.h``, which states
+what each computes) and only marshal arguments: 2-D torch tensors with unit
+stride along a row (any row stride; the matrices that a product reads need
+16-byte aligned rows), 1-D contiguous vectors, the current CUDA stream.  The
+caller owns every output and workspace.  Wrong shapes, types, devices or
+strides raise ValueError here; everything else is checked by the library and
+raises QtaError.
+
+    d = linear_desc(rows, n_out, n_in, "bf16", act="gelu_tanh")
+    qta_linear(d, x, w, y, bias=b)                          # y = gelu(x w^T + b)
+    ws = alloc_workspace(linear_bwd_workspace_bytes(d))
+    qta_linear_bwd(d, dy, x, w, dx, dw, ws, bias=b, dbias=db)
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import BF16, FP16, FP32, _check, _stream, lib
+
+NORM_LAYER, NORM_RMS = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = range(5)
+
+NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF}
+DTYPES = {"bf16": BF16, "fp16": FP16, "fp32": FP32, torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+_TORCH = {BF16: torch.bfloat16, FP16: torch.float16, FP32: torch.float32}
+
+
+class Mat(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_out", ctypes.c_int64), ("n_in", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class FfnDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+_bound = False
+
+
+def _lib():
+    """The library with the argument types of these calls set."""
+    global _bound
+    L = lib()
+    if not _bound:
+        vp, PM = ctypes.c_void_p, ctypes.POINTER(Mat)
+        PN, PL, PF = ctypes.POINTER(NormDesc), ctypes.POINTER(LinearDesc), ctypes.POINTER(FfnDesc)
+        L.qta_norm.argtypes = [PN, PM, PM, vp, vp, PM, PM, vp, vp, vp]
+        L.qta_norm_bwd.argtypes = [PN, PM, PM, vp, vp, vp, PM, PM, vp, vp, vp, vp]
+        L.qta_linear.argtypes = [PL, PM, PM, vp, PM, PM, vp]
+        L.qta_linear_bwd.argtypes = [PL, PM, PM, PM, vp, PM, PM, vp, vp, vp]
+        L.qta_gated_ffn.argtypes = [PF, PM, PM, PM, PM, vp]
+        L.qta_gated_ffn_bwd.argtypes = [PF, PM, PM, PM, PM, PM, PM, PM, vp, vp]
+        for name in ("qta_norm", "qta_norm_bwd", "qta_linear", "qta_linear_bwd", "qta_gated_ffn",
+                     "qta_gated_ffn_bwd"):
+            getattr(L, name).restype = ctypes.c_int
+        for name, t in (("qta_norm_bwd_workspace_bytes", PN), ("qta_linear_bwd_workspace_bytes", PL),
+                        ("qta_gated_ffn_bwd_workspace_bytes", PF)):
+            getattr(L, name).argtypes = [t]
+            getattr(L, name).restype = ctypes.c_size_t
+        _bound = True
+    return L
+
+
+def _pick(table, v):
+    if v in table:
+        return table[v]
+    if isinstance(v, int) and not isinstance(v, bool):
+        return v   # the library checks it
+    raise ValueError(f"unknown name {v!r}: one of {[k for k in table if isinstance(k, str)]}")
+
+
+def norm_desc(rows: int, cols: int, dtype, kind="layer", eps: float = 1e-5, w_dtype=None) -> NormDesc:
+    """dtype: of the activations; w_dtype: of gamma and beta (dtype or "fp32")."""
+    dt = _pick(DTYPES, dtype)
+    return NormDesc(rows, cols, dt, dt if w_dtype is None else _pick(DTYPES, w_dtype), _pick(NORMS, kind), eps)
+
+
+def linear_desc(rows: int, n_out: int, n_in: int, dtype, act="none", out_dtype=None, bias_dtype=None,
+                grad_dtype=None) -> LinearDesc:
+    """dtype: of x, w and their 16-bit gradients; out_dtype (y, residual), bias_dtype and grad_dtype (dw): dtype
+    or "fp32"."""
+    dt = _pick(DTYPES, dtype)
+    o, b, g = (dt if t is None else _pick(DTYPES, t) for t in (out_dtype, bias_dtype, grad_dtype))
+    return LinearDesc(rows, n_out, n_in, dt, o, b, g, _pick(ACTS, act))
+
+
+def ffn_desc(rows: int, hidden: int, width: int, dtype, act="silu", grad_dtype=None) -> FfnDesc:
+    """dtype: of x, the weights and h; grad_dtype (dwg, dwu): dtype or "fp32"."""
+    dt = _pick(DTYPES, dtype)
+    return FfnDesc(rows, hidden, width, dt, dt if grad_dtype is None else _pick(DTYPES, grad_dtype), _pick(ACTS, act))
+
+
+def norm_bwd_workspace_bytes(d: NormDesc) -> int:
+    return _lib().qta_norm_bwd_workspace_bytes(d)
+
+
+def linear_bwd_workspace_bytes(d: LinearDesc) -> int:
+    return _lib().qta_linear_bwd_workspace_bytes(d)
+
+
+def gated_ffn_bwd_workspace_bytes(d: FfnDesc) -> int:
+    return _lib().qta_gated_ffn_bwd_workspace_bytes(d)
+
+
+def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
+    """A device byte buffer (never empty, so that its address is valid)."""
+    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------- arguments
+def _mat(name, t, rows, cols, dt):
+    """A [rows, cols] tensor as a C matrix; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not _TORCH.get(dt) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor of {_TORCH.get(dt)} is needed, got {t.dtype} on {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: shape [{rows}, {cols}] is needed, got {list(t.shape)}")
+    sr, sc = t.stride()
+    if sc != 1 and cols > 1:
+        raise ValueError(f"{name}: unit stride along the rows is needed, got strides {(sr, sc)}")
+    if rows > 1 and sr < cols:
+        raise ValueError(f"{name}: rows overlap (strides {(sr, sc)})")
+    return Mat(t.data_ptr(), sr if rows > 1 else 0)
+
+
+def _vec(name, t, n, dt):
+    if t is None:
+        return None
+    if t.dtype is not _TORCH.get(dt) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor of {_TORCH.get(dt)} is needed, got {t.dtype} on {t.device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous elements are needed, got shape {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _work(t, need):
+    if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"ws: a contiguous CUDA buffer of at least {need} bytes is needed")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------- the calls
+def qta_norm(d: NormDesc, x, gamma, y, beta=None, residual=None, sum_out=None, mean=None, rstd=None,
+             stream=None) -> None:
+    """y = norm(x + residual) gamma + beta; sum_out, mean and rstd (optional) are what the backward pass needs."""
+    R, C, dt = d.rows, d.cols, d.dtype
+    _check("qta_norm", _lib().qta_norm(
+        d, _mat("x", x, R, C, dt), _mat("residual", residual, R, C, dt), _vec("gamma", gamma, C, d.w_dtype),
+        _vec("beta", beta, C, d.w_dtype), _mat("y", y, R, C, dt), _mat("sum_out", sum_out, R, C, dt),
+        _vec("mean", mean, R, FP32), _vec("rstd", rstd, R, FP32), _stream(stream)))
+
+
+def qta_norm_bwd(d: NormDesc, dy, s, gamma, rstd, dx, dgamma, ws, mean=None, dbeta=None, dsum=None,
+                 stream=None) -> None:
+    """Gradients of qta_norm: s is what was normalised (sum_out, or x where there was no residual)."""
+    R, C, dt = d.rows, d.cols, d.dtype
+    _check("qta_norm_bwd", _lib().qta_norm_bwd(
+        d, _mat("dy", dy, R, C, dt), _mat("s", s, R, C, dt), _vec("gamma", gamma, C, d.w_dtype),
+        _vec("mean", mean, R, FP32), _vec("rstd", rstd, R, FP32), _mat("dsum", dsum, R, C, dt),
+        _mat("dx", dx, R, C, dt), _vec("dgamma", dgamma, C, FP32), _vec("dbeta", dbeta, C, FP32),
+        _work(ws, norm_bwd_workspace_bytes(d)), _stream(stream)))
+
+
+def qta_linear(d: LinearDesc, x, w, y, bias=None, residual=None, stream=None) -> None:
+    """y = act(x w^T + bias) + residual."""
+    R, N, K = d.rows, d.n_out, d.n_in
+    _check("qta_linear", _lib().qta_linear(
+        d, _mat("x", x, R, K, d.dtype), _mat("w", w, N, K, d.dtype), _vec("bias", bias, N, d.bias_dtype),
+        _mat("residual", residual, R, N, d.out_dtype), _mat("y", y, R, N, d.out_dtype), _stream(stream)))
+
+
+def qta_linear_bwd(d: LinearDesc, dy, x, w, dx, dw, ws, bias=None, dbias=None, stream=None) -> None:
+    """Gradients of qta_linear; dx, dw and dbias may be None (not computed)."""
+    R, N, K = d.rows, d.n_out, d.n_in
+    _check("qta_linear_bwd", _lib().qta_linear_bwd(
+        d, _mat("dy", dy, R, N, d.dtype), _mat("x", x, R, K, d.dtype), _mat("w", w, N, K, d.dtype),
+        _vec("bias", bias, N, d.bias_dtype), _mat("dx", dx, R, K, d.dtype), _mat("dw", dw, N, K, d.grad_dtype),
+        _vec("dbias", dbias, N, FP32), _work(ws, linear_bwd_workspace_bytes(d)), _stream(stream)))
+
+
+def qta_gated_ffn(d: FfnDesc, x, wg, wu, h, stream=None) -> None:
+    """h = act(x wg^T) * (x wu^T)."""
+    R, H, F, dt = d.rows, d.hidden, d.width, d.dtype
+    _check("qta_gated_ffn", _lib().qta_gated_ffn(
+        d, _mat("x", x, R, H, dt), _mat("wg", wg, F, H, dt), _mat("wu", wu, F, H, dt), _mat("h", h, R, F, dt),
+        _stream(stream)))
+
+
+def qta_gated_ffn_bwd(d: FfnDesc, dh, x, wg, wu, dx, dwg, dwu, ws, stream=None) -> None:
+    """Gradients of qta_gated_ffn; dx, or dwg and dwu together, may be None (not computed)."""
+    R, H, F, dt = d.rows, d.hidden, d.width, d.dtype
+    _check("qta_gated_ffn_bwd", _lib().qta_gated_ffn_bwd(
+        d, _mat("dh", dh, R, F, dt), _mat("x", x, R, H, dt), _mat("wg", wg, F, H, dt), _mat("wu", wu, F, H, dt),
+        _mat("dx", dx, R, H, dt), _mat("dwg", dwg, F, H, d.grad_dtype), _mat("dwu", dwu, F, H, d.grad_dtype),
+        _work(ws, gated_ffn_bwd_workspace_bytes(d)), _stream(stream)))
