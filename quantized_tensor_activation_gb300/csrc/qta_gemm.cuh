@@ -2,11 +2,14 @@
 //
 //   D[m, n] = sum_k A[m, k] B[n, k]   (FP32 accumulators in TMEM)
 //
-// with an epilogue that finishes the operator in registers.  One CTA computes
-// tiles of 128 x BN: warp 0 loads A and B in blocks of 64 contraction
-// elements by TMA into a ring of shared-memory stages, warp 1 issues
-// tcgen05.mma on them, warps 2-5 read the accumulators of the previous tile
-// (TMEM holds two) and run the epilogue.  Operands whose contraction index is
+// with an epilogue that finishes the operator in registers.  A pair of CTAs
+// (or one CTA) computes tiles of 256 (128) x BN: warp 0 loads A and B in blocks
+// of 64 contraction elements by TMA into a ring of shared-memory stages, warp
+// 1 issues tcgen05.mma on them, warps 2-5 read the accumulators of the
+// previous tile (TMEM holds two) and run the epilogue.  In a pair each CTA
+// loads and keeps half of B, so a byte of shared memory feeds twice the
+// products that it feeds in a single CTA: the single CTA's 128 x 128 tile is
+// bound by shared memory.  Operands whose contraction index is
 // not the contiguous one (the backward products) are read as they lie, with
 // MN-major descriptors: nothing is transposed in memory.
 //
@@ -48,19 +51,36 @@ struct GemmParams {
     unsigned int* err;
 };
 
-constexpr int GEMM_BM = 128;
+constexpr int GEMM_BM = 128;   // rows of one CTA's share of a tile
 constexpr int GEMM_BK = 64;
 constexpr int GEMM_THREADS = 192;
 
-template <int BN>
+// CG CTAs compute one tile of CG * 128 x BN; each holds its 128 rows of A and
+// its BN / CG rows of B.
+template <int CG, int BN>
 struct GemmCfg {
+    static constexpr int BN_CTA = BN / CG;
     static constexpr int A_BYTES = GEMM_BM * GEMM_BK * 2;
-    static constexpr int B_BYTES = BN * GEMM_BK * 2;
+    static constexpr int B_BYTES = BN_CTA * GEMM_BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = 6;
     static constexpr int SMEM = STAGES * STAGE + 1024;   // + slack to start on 1024 bytes
     static constexpr uint32_t TMEM_COLS = 2 * BN;        // two accumulators
 };
+
+// Tiles in an order that keeps a wave of CTAs on few rows and columns of
+// tiles: GROUP_M row tiles side by side, all column tiles of them, then the
+// next rows.  What a wave reads then stays in L2 while its CTAs share it.
+constexpr int GROUP_M = 8;
+
+__device__ __forceinline__ void tile_coords(int r, int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int band = r / (GROUP_M * tiles_n), first = band * GROUP_M;
+    const int height = min(GROUP_M, tiles_m - first);
+    const int in = r - band * GROUP_M * tiles_n;
+    tm = first + in % height;
+    tn = in / height;
+}
 
 // 32 elements of one row from column c0 on, n of them in range.
 __device__ __forceinline__ void row_load32(const void* base, int64_t off, int dt, int n, float (&v)[32])
@@ -138,10 +158,10 @@ __device__ __forceinline__ float column_sum32(float (&v)[32], int lane)
     return v[0];
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p)
+template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p)
 {
-    using C = GemmCfg<BN>;
+    using C = GemmCfg<CG, BN>;
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
     constexpr int TILE_N = DUAL ? BN / 2 : BN;   // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
@@ -151,6 +171,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -159,14 +181,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], 4 * CG);
         }
         mbar_init(&drain, 1);
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(&tmem_slot, C::TMEM_COLS);
+    __syncwarp();
+    if (warp == 1) tmem_alloc<CG>(&tmem_slot, C::TMEM_COLS);
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();   // the barriers of both CTAs exist before either signals the other
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
@@ -180,9 +206,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             int s = 0, done = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+            for (int t = first; ok && t < n_tiles; t += step) {
                 const int g = t / per_group, r = t - g * per_group;
-                const int m0 = (r % p.tiles_m) * GEMM_BM, n0 = (r / p.tiles_m) * TILE_N;
+                int tm, tn;
+                tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
+                const int m0 = (tm * CG + rank) * GEMM_BM, n0 = tn * TILE_N;
+                const int nb = DUAL ? n0 : n0 + rank * C::BN_CTA;   // this CTA's rows of B
                 for (int kb = 0; kb < p.nk; ++kb) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) {
                         ok = false;
@@ -194,21 +223,29 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     const CUtensorMap* mb = &p.b[second];
                     uint8_t* sa = smem + s * C::STAGE;
                     uint8_t* sb = sa + C::A_BYTES;
-                    mbar_arrive_expect_tx(&full[s], C::STAGE);
+                    auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
+                        if constexpr (CG == 2)
+                            tma_load_2d_pair(dst, map, c0, c1, leader_addr(&full[s]));
+                        else
+                            tma_load_2d(dst, map, c0, c1, &full[s]);
+                    };
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE);
                     if constexpr (A_MN) {
-                        for (int i = 0; i < GEMM_BM / 64; ++i)
-                            tma_load_2d(sa + i * BOX_BYTES, ma, m0 + 64 * i, k0, &full[s]);
+#pragma unroll
+                        for (int i = 0; i < GEMM_BM / 64; ++i) load(sa + i * BOX_BYTES, ma, m0 + 64 * i, k0);
                     } else {
-                        tma_load_2d(sa, ma, k0, m0, &full[s]);
+                        load(sa, ma, k0, m0);
                     }
-                    if constexpr (DUAL) {
-                        tma_load_2d(sb, &p.b[0], k0, n0, &full[s]);
-                        tma_load_2d(sb + C::B_BYTES / 2, &p.b[1], k0, n0, &full[s]);
+                    if constexpr (DUAL && CG == 2) {
+                        load(sb, &p.b[rank], k0, nb);
+                    } else if constexpr (DUAL) {
+                        load(sb, &p.b[0], k0, nb);
+                        load(sb + C::B_BYTES / 2, &p.b[1], k0, nb);
                     } else if constexpr (B_MN) {
-                        for (int i = 0; i < BN / 64; ++i)
-                            tma_load_2d(sb + i * BOX_BYTES, mb, n0 + 64 * i, k0, &full[s]);
+#pragma unroll
+                        for (int i = 0; i < C::BN_CTA / 64; ++i) load(sb + i * BOX_BYTES, mb, nb + 64 * i, k0);
                     } else {
-                        tma_load_2d(sb, mb, k0, n0, &full[s]);
+                        load(sb, mb, k0, nb);
                     }
                     ++done;
                     if (++s == C::STAGES) {
@@ -217,7 +254,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     }
                 }
             }
-            if (!ok) {   // let the loads in flight land before the shared memory goes away
+            // let the loads in flight land before the shared memory goes away (with a pair, the even CTA's barriers
+            // count both CTAs' loads, and neither leaves before both are here)
+            if (!ok && rank == 0) {
                 const int n = done < C::STAGES ? done : C::STAGES;
                 const uint64_t until = globaltimer_ns() + 2000000000ull;
                 for (int i = 1; i <= n; ++i) {
@@ -227,13 +266,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             int s = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x, ++it) {
+            for (int t = first; ok && t < n_tiles; t += step, ++it) {
                 const int buf = it & 1;
-                if (!mbar_wait(&acc_empty[buf], ((it >> 1) & 1) ^ 1u, p.err)) {
+                const uint32_t drained = ((it >> 1) & 1) ^ 1u;
+                if (!(CG == 2 ? mbar_wait_cluster(&acc_empty[buf], drained, p.err)
+                              : mbar_wait(&acc_empty[buf], drained, p.err))) {
                     ok = false;
                     break;
                 }
@@ -248,18 +289,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * C::STAGE + C::A_BYTES));
 #pragma unroll
                     for (int k = 0; k < GEMM_BK / 16; ++k)
-                        tc_mma(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
+                        tc_mma<CG>(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
                                kb > 0 || k > 0);
-                    tc_commit(&empty[s]);
+                    tc_commit<CG>(&empty[s]);
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (ok) tc_commit(&acc_full[buf]);
+                if (ok) tc_commit<CG>(&acc_full[buf]);
             }
             if (!ok) {   // the products in flight end before TMEM is freed
-                tc_commit(&drain);
+                tc_commit<CG>(&drain);
                 mbar_wait_until(&drain, 0, globaltimer_ns() + 2000000000ull);
             }
         }
@@ -267,10 +308,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         const int q = warp & 3;   // the TMEM lanes (rows) this warp may read: 32 q ...
         int it = 0;
         bool ok = true;   // after an expired wait a warp still takes part in the barriers below, without work
-        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++it) {
+        for (int t = first; t < n_tiles; t += step, ++it) {
             const int buf = it & 1;
             const int g = t / per_group, r = t - g * per_group;
-            const int m0 = (r % p.tiles_m) * GEMM_BM, n0 = (r / p.tiles_m) * TILE_N;
+            int tm, tn;
+            tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
+            const int m0 = (tm * CG + rank) * GEMM_BM, n0 = tn * TILE_N;
             const int row = m0 + 32 * q + lane;
             const bool live = row < p.M;
             const int64_t row64 = row;
@@ -350,12 +393,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            if (lane == 0) {
+                if constexpr (CG == 2)
+                    mbar_arrive_cluster(leader_addr(&acc_empty[buf]));
+                else
+                    mbar_arrive(&acc_empty[buf]);
+            }
             if constexpr (EPI == EPI_LINEAR_BWD) {
                 if (p.colsum) {   // the four warps' sums, in warp order
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     for (int c = threadIdx.x - 64; c < BN; c += 128)
-                        if (n0 + c < p.N)
+                        if (n0 + c < p.N && m0 < p.M)
                             p.colsum[static_cast<int64_t>(m0 / GEMM_BM) * p.N + n0 + c] =
                                 (colsum_s[c] + colsum_s[BN + c]) + (colsum_s[2 * BN + c] + colsum_s[3 * BN + c]);
                     asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -363,10 +411,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
         }
     }
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == 1) tmem_dealloc<CG>(tmem, C::TMEM_COLS);
 }
 
 }  // namespace qta

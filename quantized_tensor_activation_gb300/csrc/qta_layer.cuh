@@ -18,8 +18,12 @@ cudaError_t launch_col_finish(const float* part, int64_t stride, int parts, int6
 // (forward), B contiguous along its output index (dx = dz w), both (dw = dz^T x).
 enum GemmForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 
-// Output columns of a tile of gemm_kernel for the given problem.
-int gemm_tile_cols(int form, int epi);
-cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
+// Tile of a product: output rows and columns, rows of the TMA box of a
+// contraction-contiguous B, CTAs that share it, columns of its accumulator.
+struct GemmTile {
+    int rows, cols, b_box, cg, bn;
+};
+GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int groups, int sms);
+cudaError_t launch_gemm(int form, int epi, const GemmTile& t, const GemmParams& p, int sms, cudaStream_t stream);
 
 }  // namespace qta

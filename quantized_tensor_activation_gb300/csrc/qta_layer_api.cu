@@ -160,9 +160,9 @@ qta_status run_gemm(int form, int epi, GemmParams& p, int32_t dt, const View* a0
     int sms = 0;
     if (query_device(&sms, &p.err) != cudaSuccess) return QTA_ERR_CUDA;
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const int tile_n = gemm_tile_cols(form, epi);
+    const GemmTile t = gemm_tile(form, epi, M, N, groups, sms);
     const int a_rows = form == FORM_TN ? 64 : GEMM_BM;
-    const int b_rows = form == FORM_NT ? tile_n : 64;
+    const int b_rows = form == FORM_NT ? t.b_box : 64;
     if (!map_mat(&p.a[0], *a0, a_rows) || !map_mat(&p.b[0], *b0, b_rows)) return QTA_ERR_CUDA;
     if (a1 && !map_mat(&p.a[1], *a1, a_rows)) return QTA_ERR_CUDA;
     if (b1 && !map_mat(&p.b[1], *b1, b_rows)) return QTA_ERR_CUDA;
@@ -170,12 +170,12 @@ qta_status run_gemm(int form, int epi, GemmParams& p, int32_t dt, const View* a0
     p.N = static_cast<int>(N);
     p.nk0 = p.nk = static_cast<int>(ceil_div(K, GEMM_BK));
     if (a1 && groups == 1 && !dual) p.nk *= 2;
-    p.tiles_m = static_cast<int>(ceil_div(M, GEMM_BM));
-    p.tiles_n = static_cast<int>(ceil_div(N, tile_n));
+    p.tiles_m = static_cast<int>(ceil_div(M, t.rows));
+    p.tiles_n = static_cast<int>(ceil_div(N, t.cols));
     p.groups = groups;
     if (static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups >= (int64_t(1) << 31)) return QTA_ERR_UNSUPPORTED;
     p.idesc = idesc_f16(0, 0, dt == QTA_BF16, false, false);   // the launcher adds the tile
-    return cuda_status(launch_gemm(form, epi, p, sms, s));
+    return cuda_status(launch_gemm(form, epi, t, p, sms, s));
 }
 
 GemmParams blank()
