@@ -49,44 +49,56 @@ __device__ __forceinline__ float gelu_tanh_2q(float z)
     return z * fmaf(0.0713548162726009f, z * z, 1.5957691216057308f);
 }
 
-__device__ __forceinline__ float act_value(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float act_value(float z)
 {
-    switch (act) {
-    case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case ACT_SILU: return z * sigmoid_fast(z);
-    case ACT_GELU_TANH: return z * sigmoid_fast(gelu_tanh_2q(z));
-    case ACT_GELU_ERF: return 0.5f * z * erfcf(-0.7071067811865476f * z);   // no cancellation for z << 0
-    default: return z;
-    }
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == ACT_SILU) return z * sigmoid_fast(z);
+    if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid_fast(gelu_tanh_2q(z));
+    if constexpr (ACT == ACT_GELU_ERF) return 0.5f * z * erfcf(-0.7071067811865476f * z);   // no cancellation for z << 0
+    return z;
 }
 
 // f(z) and f'(z).
-__device__ __forceinline__ void act_both(float z, int act, float& f, float& df)
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& f, float& df)
 {
-    switch (act) {
-    case ACT_RELU:
-        f = z > 0.0f ? z : (z != z ? z : 0.0f);
+    f = z;
+    df = 1.0f;
+    if constexpr (ACT == ACT_RELU) {
+        f = act_value<ACT_RELU>(z);
         df = z > 0.0f ? 1.0f : 0.0f;
-        return;
-    case ACT_SILU: {
+    } else if constexpr (ACT == ACT_SILU) {
         const float p = sigmoid_fast(z);
         f = z * p;
         df = fmaf(f, 1.0f - p, p);
-        return;
-    }
-    case ACT_GELU_TANH: {
+    } else if constexpr (ACT == ACT_GELU_TANH) {
         const float p = sigmoid_fast(gelu_tanh_2q(z));
         f = z * p;
         df = fmaf(f * (1.0f - p), fmaf(0.2140644488178027f, z * z, 1.5957691216057308f), p);
-        return;
-    }
-    case ACT_GELU_ERF: {
+    } else if constexpr (ACT == ACT_GELU_ERF) {
         const float c = 0.5f * erfcf(-0.7071067811865476f * z);
         f = z * c;
         df = fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), c);
-        return;
     }
-    default: f = z; df = 1.0f; return;
+}
+
+// Calls f with the activation as a compile-time constant: the branch is taken
+// once for many elements.
+template <int A>
+struct ActTag {
+    static constexpr int value = A;
+};
+
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f)
+{
+    switch (act) {
+    case ACT_RELU: f(ActTag<ACT_RELU>{}); break;
+    case ACT_SILU: f(ActTag<ACT_SILU>{}); break;
+    case ACT_GELU_TANH: f(ActTag<ACT_GELU_TANH>{}); break;
+    case ACT_GELU_ERF: f(ActTag<ACT_GELU_ERF>{}); break;
+    default: f(ActTag<ACT_NONE>{}); break;
     }
 }
 

@@ -5,7 +5,7 @@
 // with an epilogue that finishes the operator in registers.  A pair of CTAs
 // (or one CTA) computes tiles of 256 (128) x BN: warp 0 loads A and B in blocks
 // of 64 contraction elements by TMA into a ring of shared-memory stages, warp
-// 1 issues tcgen05.mma on them, warps 2-5 read the accumulators of the
+// 1 issues tcgen05.mma on them, warps 2-9 read the accumulators of the
 // previous tile (TMEM holds two) and run the epilogue.  In a pair each CTA
 // loads and keeps half of B, so a byte of shared memory feeds twice the
 // products that it feeds in a single CTA: the single CTA's 128 x 128 tile is
@@ -47,13 +47,19 @@ struct GemmParams {
     void* out[2];
     int64_t ld_out[2];
     int out_dt;
-    float* colsum;              // EPI_LINEAR_BWD: [tiles_m][N] partial column sums (NULL: none)
+    float* colsum;              // EPI_LINEAR_BWD: [ceil(M / 32)][N] partial column sums (NULL: none)
+    // aux and out pass through shared memory by TMA (16-byte aligned rows), in
+    // boxes of 32 rows x epi_box_cols; else by per-thread loads and stores
+    int staged;
+    CUtensorMap aux_map, out_map[2];
     unsigned int* err;
 };
 
 constexpr int GEMM_BM = 128;   // rows of one CTA's share of a tile
 constexpr int GEMM_BK = 64;
-constexpr int GEMM_THREADS = 192;
+constexpr int GEMM_EPI_WARPS = 8;
+constexpr int GEMM_THREADS = 64 + 32 * GEMM_EPI_WARPS;
+constexpr int EPI_BUF = 4096;   // staging bytes of an epilogue warp: 32 rows x 128 bytes
 
 // CG CTAs compute one tile of CG * 128 x BN; each holds its 128 rows of A and
 // its BN / CG rows of B.
@@ -64,9 +70,17 @@ struct GemmCfg {
     static constexpr int B_BYTES = BN_CTA * GEMM_BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = 6;
-    static constexpr int SMEM = STAGES * STAGE + 1024;   // + slack to start on 1024 bytes
+    static constexpr int SMEM = STAGES * STAGE + GEMM_EPI_WARPS * EPI_BUF + 1024;   // + slack to start on 1024 bytes
     static constexpr uint32_t TMEM_COLS = 2 * BN;        // two accumulators
 };
+
+// Columns that an epilogue warp stages at a time: rows of 128 bytes, or of 64
+// where its buffer holds two outputs or its share of the tile is 32 columns.
+__host__ __device__ constexpr int epi_box_cols(int epi, int bn, bool fp32)
+{
+    const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
+    return fp32 || epi == EPI_GATED_BWD || (dual ? bn / 4 : bn / 2) < 64 ? 32 : 64;
+}
 
 // Tiles in an order that keeps a wave of CTAs on few rows and columns of
 // tiles: GROUP_M row tiles side by side, all column tiles of them, then the
@@ -82,34 +96,70 @@ __device__ __forceinline__ void tile_coords(int r, int tiles_m, int tiles_n, int
     tn = in / height;
 }
 
-// 32 elements of one row from column c0 on, n of them in range.
+// Eight 16-bit elements and back; the branch on the type is the caller's.
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4 w, float* v)
+{
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2(ws[j], DT);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float* v)
+{
+    return make_uint4(pack2(v[0], v[1], DT), pack2(v[2], v[3], DT), pack2(v[4], v[5], DT), pack2(v[6], v[7], DT));
+}
+
+// The 16-byte pieces at(0), at(1), ... of 32 elements of type dt.
+template <typename At>
+__device__ __forceinline__ void get32(int dt, float (&v)[32], At&& at)
+{
+    if (dt == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 w = *at(i);
+            v[4 * i] = __uint_as_float(w.x);
+            v[4 * i + 1] = __uint_as_float(w.y);
+            v[4 * i + 2] = __uint_as_float(w.z);
+            v[4 * i + 3] = __uint_as_float(w.w);
+        }
+    } else if (dt == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack8<0>(*at(i), v + 8 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack8<1>(*at(i), v + 8 * i);
+    }
+}
+
+template <typename At>
+__device__ __forceinline__ void put32(int dt, const float (&v)[32], At&& at)
+{
+    if (dt == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *at(i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                __float_as_uint(v[4 * i + 3]));
+    } else if (dt == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *at(i) = pack8<0>(v + 8 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *at(i) = pack8<1>(v + 8 * i);
+    }
+}
+
+// 32 elements of one row from element `off` on, n of them in range.
 __device__ __forceinline__ void row_load32(const void* base, int64_t off, int dt, int n, float (&v)[32])
 {
     const uint8_t* p = static_cast<const uint8_t*>(base) + off * dt_size(dt);
     if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-        if (dt == 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 w = q[i];
-                v[4 * i] = __uint_as_float(w.x);
-                v[4 * i + 1] = __uint_as_float(w.y);
-                v[4 * i + 2] = __uint_as_float(w.z);
-                v[4 * i + 3] = __uint_as_float(w.w);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 w = q[i];
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack2(ws[j], dt);
-                    v[8 * i + 2 * j] = f.x;
-                    v[8 * i + 2 * j + 1] = f.y;
-                }
-            }
-        }
+        get32(dt, v, [&](int i) { return reinterpret_cast<const uint4*>(p) + i; });
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = i < n ? load_elem(p, i, dt) : 0.0f;
@@ -120,18 +170,7 @@ __device__ __forceinline__ void row_store32(void* base, int64_t off, int dt, int
 {
     uint8_t* p = static_cast<uint8_t*>(base) + off * dt_size(dt);
     if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        uint4* q = reinterpret_cast<uint4*>(p);
-        if (dt == 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                q[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                q[i] = make_uint4(pack2(v[8 * i], v[8 * i + 1], dt), pack2(v[8 * i + 2], v[8 * i + 3], dt),
-                                  pack2(v[8 * i + 4], v[8 * i + 5], dt), pack2(v[8 * i + 6], v[8 * i + 7], dt));
-        }
+        put32(dt, v, [&](int i) { return reinterpret_cast<uint4*>(p) + i; });
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -166,8 +205,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
     constexpr int TILE_N = DUAL ? BN / 2 : BN;   // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t aux_full[GEMM_EPI_WARPS];
     __shared__ uint32_t tmem_slot;
-    __shared__ float colsum_s[EPI == EPI_LINEAR_BWD ? 4 * BN : 1];
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,8 +220,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4 * CG);
+            mbar_init(&acc_empty[i], GEMM_EPI_WARPS * CG);
         }
+        for (int i = 0; i < GEMM_EPI_WARPS; ++i) mbar_init(&aux_full[i], 1);
         mbar_init(&drain, 1);
         fence_barrier_init();
     }
@@ -305,111 +345,151 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
             }
         }
     } else {
-        const int q = warp & 3;   // the TMEM lanes (rows) this warp may read: 32 q ...
+        // Epilogue warps: each has 32 rows (the TMEM lanes its index mod 4 may
+        // read) and half of the tile's columns, in pieces of 32.  Staged, aux
+        // arrives in the warp's buffer by TMA (the first box before the
+        // accumulators are ready), each lane replaces its own row by the
+        // output, and the box leaves by TMA: full lines, and a quarter of the
+        // shared-memory and L1 cycles of 16-byte accesses to 32 rows, which
+        // the operand ring needs.
+        constexpr int HALF = TILE_N / 2;
+        const int q = warp & 3, ew = warp - 2, half = ew >> 2;
+        const bool f32 = p.out_dt == 2;
+        const int box = epi_box_cols(EPI, BN, f32);
+        const int row_bytes = (f32 || box == 64) ? 128 : 64;
+        const uint32_t box_bytes = 32u * row_bytes;
+        uint8_t* buf = smem + C::STAGES * C::STAGE + ew * EPI_BUF;
+        uint8_t* buf2 = buf + EPI_BUF / 2;   // EPI_GATED_BWD: the second output
+        uint32_t aux_ph = 0;
         int it = 0;
-        bool ok = true;   // after an expired wait a warp still takes part in the barriers below, without work
+        bool ok = true;   // after an expired wait a warp goes on without work
         for (int t = first; t < n_tiles; t += step, ++it) {
-            const int buf = it & 1;
+            const int ab = it & 1;
             const int g = t / per_group, r = t - g * per_group;
             int tm, tn;
             tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
-            const int m0 = (tm * CG + rank) * GEMM_BM, n0 = tn * TILE_N;
-            const int row = m0 + 32 * q + lane;
+            const int row0 = (tm * CG + rank) * GEMM_BM + 32 * q, n0 = tn * TILE_N + half * HALF;
+            const int row = row0 + lane;
             const bool live = row < p.M;
             const int64_t row64 = row;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1, p.err));
+            // the warp's buffer is free again; aux of the columns from c on
+            auto refill = [&](int c) {
+                if (lane == 0) {
+                    bulk_wait_read<0>();
+                    if (p.aux && row0 < p.M && n0 + c < p.N) {
+                        mbar_arrive_expect_tx(&aux_full[ew], box_bytes);
+                        tma_load_2d(buf, &p.aux_map, n0 + c, row0, &aux_full[ew]);
+                    }
+                }
+                __syncwarp();
+            };
+            // 16-byte piece i of this lane's row, for the 32 columns from c on
+            auto at = [&](uint8_t* b, int c, int i) {
+                const uint32_t k = static_cast<uint32_t>(i) + (row_bytes == 128 && !f32 && (c & 32) ? 4u : 0u);
+                return reinterpret_cast<uint4*>(b + (row_bytes == 128 ? sw128(lane, k) : sw64(lane, k)));
+            };
+            if (p.staged && ok) refill(0);   // (an aux box lands within the two seconds of an expired wait)
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (it >> 1) & 1, p.err));
             tc_fence_after();
-            const uint32_t acc = tmem + buf * BN + (static_cast<uint32_t>(32 * q) << 16);
+            const uint32_t acc = tmem + ab * BN + half * HALF + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll 1
-            for (int c = 0; ok && c < TILE_N; c += 32) {
+            for (int c = 0; ok && c < HALF; c += 32) {
                 const int col = n0 + c;
                 const int n = p.N - col;   // columns in range (may be <= 0)
-                float v[32];
+                const bool some = n > 0 && row0 < p.M;
+                float v[32], u[DUAL ? 32 : 1];
                 tmem_ld32(acc + c, v);
-                if constexpr (EPI == EPI_LINEAR) {
-                    tmem_ld_wait();
-                    if (n > 0) {
+                if constexpr (DUAL) tmem_ld32(acc + TILE_N + c, u);
+                tmem_ld_wait();
+                if (c + 32 >= HALF) {   // the accumulators have been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            mbar_arrive_cluster(leader_addr(&acc_empty[ab]));
+                        else
+                            mbar_arrive(&acc_empty[ab]);
+                    }
+                }
+                float x[32];
+                if (p.aux && some) {
+                    if (p.staged) {
+                        if ((c & (box - 1)) == 0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(&aux_full[ew], aux_ph, p.err));
+                            aux_ph ^= 1u;
+                            if (!ok) break;
+                        }
+                        get32(p.aux_dt, x, [&](int i) { return at(buf, c, i); });
+                    } else if (live) {
+                        row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
+                    }
+                }
+                if (some) {
+                    if constexpr (!DUAL) {
                         if (p.bias) {
+                            float b[32];
+                            row_load32(p.bias, col, p.bias_dt, n, b);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < n) v[i] += load_elem(p.bias, col + i, p.bias_dt);
-                        }
-                        if (p.act != ACT_NONE) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], p.act);
-                        }
-                        if (live) {
-                            if (p.aux) {
-                                float res[32];
-                                row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, res);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] += res[i];
-                            }
-                            row_store32(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
+                            for (int i = 0; i < 32; ++i) v[i] += b[i];
                         }
                     }
-                } else if constexpr (EPI == EPI_LINEAR_BWD) {
-                    tmem_ld_wait();
-                    float dy[32];
-                    if (live && n > 0) {
-                        row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, dy);
+                    with_act(p.act, [&](auto tag) {
+                        constexpr int ACT = decltype(tag)::value;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            float f, df;
-                            const float z = v[i] + (p.bias && i < n ? load_elem(p.bias, col + i, p.bias_dt) : 0.0f);
-                            act_both(z, p.act, f, df);
-                            v[i] = i < n ? dy[i] * df : 0.0f;
-                        }
-                        row_store32(p.out[0], row64 * p.ld_out[0] + col, p.out_dt, n, v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    }
-                    if (p.colsum) colsum_s[q * BN + c + lane] = column_sum32(v, lane);
-                } else {
-                    float u[32];
-                    tmem_ld32(acc + TILE_N + c, u);
-                    tmem_ld_wait();
-                    if (live && n > 0) {
-                        if constexpr (EPI == EPI_GATED) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], p.act) * u[i];
-                            row_store32(p.out[0], row64 * p.ld_out[0] + col, p.out_dt, n, v);
-                        } else {
-                            float dh[32];
-                            row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, dh);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
+                            if constexpr (EPI == EPI_LINEAR) {
+                                v[i] = act_value<ACT>(v[i]);
+                            } else if constexpr (EPI == EPI_GATED) {
+                                v[i] = act_value<ACT>(v[i]) * u[i];
+                            } else {
                                 float f, df;
-                                act_both(v[i], p.act, f, df);
-                                v[i] = dh[i] * u[i] * df;
-                                u[i] = dh[i] * f;
+                                act_both<ACT>(v[i], f, df);
+                                if constexpr (EPI == EPI_LINEAR_BWD) {
+                                    v[i] = live && i < n ? x[i] * df : 0.0f;
+                                } else {
+                                    v[i] = x[i] * u[i] * df;
+                                    u[i] = x[i] * f;
+                                }
                             }
-                            row_store32(p.out[0], row64 * p.ld_out[0] + col, p.out_dt, n, v);
+                        }
+                    });
+                    if constexpr (EPI == EPI_LINEAR) {
+                        if (p.aux) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += x[i];
+                        }
+                    }
+                    if (p.staged) {
+                        put32(p.out_dt, v, [&](int i) { return at(buf, c, i); });
+                        if constexpr (EPI == EPI_GATED_BWD) put32(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
+                    } else if (live) {
+                        row_store32(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
+                        if constexpr (EPI == EPI_GATED_BWD)
                             row_store32(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
+                    }
+                    if constexpr (EPI == EPI_LINEAR_BWD) {
+                        if (p.colsum) {
+                            const float sum = column_sum32(v, lane);
+                            if (lane < n) p.colsum[static_cast<int64_t>(row0 / 32) * p.N + col + lane] = sum;
                         }
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2)
-                    mbar_arrive_cluster(leader_addr(&acc_empty[buf]));
-                else
-                    mbar_arrive(&acc_empty[buf]);
-            }
-            if constexpr (EPI == EPI_LINEAR_BWD) {
-                if (p.colsum) {   // the four warps' sums, in warp order
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    for (int c = threadIdx.x - 64; c < BN; c += 128)
-                        if (n0 + c < p.N && m0 < p.M)
-                            p.colsum[static_cast<int64_t>(m0 / GEMM_BM) * p.N + n0 + c] =
-                                (colsum_s[c] + colsum_s[BN + c]) + (colsum_s[2 * BN + c] + colsum_s[3 * BN + c]);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (p.staged && ((c + 32) & (box - 1)) == 0) {
+                    if (n > 32 - box && row0 < p.M) {   // the box has columns in range
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int c0 = col + 32 - box;
+                            tma_store_2d(&p.out_map[g], c0, row0, buf);
+                            if constexpr (EPI == EPI_GATED_BWD) tma_store_2d(&p.out_map[1], c0, row0, buf2);
+                            bulk_commit();
+                        }
+                    }
+                    if (c + 32 < HALF) refill(c + 32);
                 }
             }
         }
+        if (lane == 0) bulk_wait_all();   // the last boxes have left this CTA's shared memory
     }
     __syncwarp();
     tc_fence_before();

@@ -54,10 +54,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // SMs of the current device and the address of its error flags.
 cudaError_t query_device(int* sms, unsigned int** err);
-// 2D tensor map of a 16-bit matrix with `ld` elements between rows: boxes of
-// box_cols (64) x box_rows, 128-byte swizzle, zeros past either end.
-bool encode_matrix16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols,
-                     uint32_t box_rows);
+// 2D tensor map of a matrix with `ld` elements between rows: boxes of
+// box_cols (64 or 128 bytes, swizzled over that width) x box_rows, zeros past
+// either end.
+bool encode_matrix(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld, int elem_bytes,
+                   uint32_t box_cols, uint32_t box_rows);
 
 // Per-device one-time setting of the dynamic shared-memory limit of a kernel.
 cudaError_t ensure_smem_attr(const void* func, int smem, std::atomic<unsigned>* done_mask);

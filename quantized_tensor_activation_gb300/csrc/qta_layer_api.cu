@@ -98,7 +98,13 @@ qta_status cuda_status(cudaError_t e) { return e == cudaSuccess ? QTA_OK : QTA_E
 // Tensor map of a 16-bit matrix: boxes of 64 columns x `box_rows` rows.
 bool map_mat(CUtensorMap* m, const View& v, int box_rows)
 {
-    return encode_matrix16(m, v.p, v.cols, v.rows, v.ld, 64, box_rows);
+    return encode_matrix(m, v.p, v.cols, v.rows, v.ld, 2, 64, box_rows);
+}
+
+// Tensor map of a matrix of the epilogue: boxes of 32 rows x `cols`.
+bool map_epi(CUtensorMap* m, const View& v, int cols)
+{
+    return encode_matrix(m, v.p, v.cols, v.rows, v.ld, v.es, cols, 32);
 }
 
 cudaError_t zero_mat(const View& v, cudaStream_t s)
@@ -151,10 +157,25 @@ qta_status check_ffn_desc(const qta_ffn_desc* d)
     return check_sizes(d->rows, d->hidden, d->width);
 }
 
+// What the epilogue reads and writes.
+struct Outs {
+    const View* out0;
+    const View* out1;
+    const View* aux;
+};
+
+// Whether TMA may load and store the matrix.  Rows have to be whole 16-byte
+// pieces too: a box that ends inside a piece is stored to that piece's end
+// (measured: 14 bytes past a row of 129 bf16 values).
+bool tma_ok(const View& v)
+{
+    return reinterpret_cast<uintptr_t>(v.p) % 16 == 0 && (v.ld * v.es) % 16 == 0 && (v.cols * v.es) % 16 == 0;
+}
+
 // One launch: D[M, N] over contraction K of a[0] and b[0] (and of a[1], b[1]
 // where given: `groups` == 1 adds their product to the same D, 2 computes a
 // second D of a[1] and b[0]).  The epilogue fields of p are the caller's.
-qta_status run_gemm(int form, int epi, GemmParams& p, int32_t dt, const View* a0, const View* a1, const View* b0,
+qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt, const View* a0, const View* a1, const View* b0,
                     const View* b1, int64_t M, int64_t N, int64_t K, int groups, cudaStream_t s)
 {
     int sms = 0;
@@ -174,6 +195,24 @@ qta_status run_gemm(int form, int epi, GemmParams& p, int32_t dt, const View* a0
     p.tiles_n = static_cast<int>(ceil_div(N, t.cols));
     p.groups = groups;
     if (static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups >= (int64_t(1) << 31)) return QTA_ERR_UNSUPPORTED;
+    p.out[0] = o.out0->w();
+    p.ld_out[0] = o.out0->ld;
+    if (o.out1) {
+        p.out[1] = o.out1->w();
+        p.ld_out[1] = o.out1->ld;
+    }
+    if (o.aux) {
+        p.aux = o.aux->p;
+        p.ld_aux = o.aux->ld;
+        p.aux_dt = p.out_dt;
+    }
+    p.staged = tma_ok(*o.out0) && (!o.out1 || tma_ok(*o.out1)) && (!o.aux || tma_ok(*o.aux));
+    if (p.staged) {
+        const int box = epi_box_cols(epi, t.bn, p.out_dt == QTA_FP32);
+        if (!map_epi(&p.out_map[0], *o.out0, box) || (o.out1 && !map_epi(&p.out_map[1], *o.out1, box)) ||
+            (o.aux && !map_epi(&p.aux_map, *o.aux, box)))
+            return QTA_ERR_CUDA;
+    }
     p.idesc = idesc_f16(0, 0, dt == QTA_BF16, false, false);   // the launcher adds the tile
     return cuda_status(launch_gemm(form, epi, t, p, sms, s));
 }
@@ -183,12 +222,6 @@ GemmParams blank()
     GemmParams p;
     std::memset(&p, 0, sizeof(p));
     return p;
-}
-
-void set_out(GemmParams& p, int i, const View& v)
-{
-    p.out[i] = v.w();
-    p.ld_out[i] = v.ld;
 }
 
 // Workspace of the backward products: 16-bit intermediates of `width`
@@ -348,19 +381,16 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     p.act = d->act;
     p.bias = bias;
     p.bias_dt = d->bias_dtype;
-    p.aux = vr.p;
-    p.ld_aux = vr.ld;
-    p.aux_dt = p.out_dt = d->out_dtype;
-    set_out(p, 0, vy);
-    return run_gemm(FORM_NT, EPI_LINEAR, p, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+    p.out_dt = d->out_dtype;
+    return run_gemm(FORM_NT, EPI_LINEAR, p, {&vy, nullptr, residual ? &vr : nullptr}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
-// Row partitions of dbias: one per 128-row tile where the epilogue sums dz,
+// Row partitions of dbias: one per 32 rows where the epilogue sums dz,
 // else those of the column sum of dy.
 static int64_t bias_parts(const qta_linear_desc* d)
 {
-    return d->act == QTA_ACT_NONE ? col_parts(d->rows) : ceil_div(d->rows, GEMM_BM);
+    return d->act == QTA_ACT_NONE ? col_parts(d->rows) : ceil_div(d->rows, 32);
 }
 
 size_t qta_linear_bwd_workspace_bytes(const qta_linear_desc* d)
@@ -408,12 +438,9 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
         p.act = d->act;
         p.bias = bias;
         p.bias_dt = d->bias_dtype;
-        p.aux = vdy.p;
-        p.ld_aux = vdy.ld;
-        p.aux_dt = p.out_dt = d->dtype;
+        p.out_dt = d->dtype;
         p.colsum = dbias ? part : nullptr;
-        set_out(p, 0, dz);
-        st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+        st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, {&dz, nullptr, &vdy}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
                       cs);
         if (st != QTA_OK) return st;
     }
@@ -427,15 +454,13 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        set_out(p, 0, vdx);
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1, cs);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1, cs);
         if (st != QTA_OK) return st;
     }
     if (dw) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        set_out(p, 0, vdw);
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1, cs);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdw, nullptr, nullptr}, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1, cs);
         if (st != QTA_OK) return st;
     }
     return QTA_OK;
@@ -460,8 +485,7 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     GemmParams p = blank();
     p.act = d->act;
     p.out_dt = d->dtype;
-    set_out(p, 0, vh);
-    return run_gemm(FORM_NT, EPI_GATED, p, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
+    return run_gemm(FORM_NT, EPI_GATED, p, {&vh, nullptr, nullptr}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
                     reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -504,27 +528,20 @@ qta_status qta_gated_ffn_bwd(const qta_ffn_desc* d, const qta_mat* dh, const qta
     {
         GemmParams p = blank();
         p.act = d->act;
-        p.aux = vdh.p;
-        p.ld_aux = vdh.ld;
-        p.aux_dt = p.out_dt = d->dtype;
-        set_out(p, 0, mg);
-        set_out(p, 1, mu);
-        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1, cs);
+        p.out_dt = d->dtype;
+        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, {&mg, &mu, &vdh}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1, cs);
         if (st != QTA_OK) return st;
     }
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        set_out(p, 0, vdx);
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1, cs);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1, cs);
         if (st != QTA_OK) return st;
     }
     if (dwg) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        set_out(p, 0, vdg);
-        set_out(p, 1, vdu);
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2, cs);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdg, &vdu, nullptr}, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2, cs);
         if (st != QTA_OK) return st;
     }
     return QTA_OK;
