@@ -7,6 +7,9 @@
 
 namespace qta {
 
+// Partial column sums of the backward passes: at most this many rows of them.
+constexpr int64_t MAX_PARTS = 304;
+
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_col_sum(const void* a, int64_t ld, int dt, int64_t rows, int64_t cols, int parts, float* part,

@@ -127,7 +127,6 @@ qta_status check_norm_desc(const qta_norm_desc* d)
 
 // Row partitions of a column sum: enough CTAs to fill the GPU, few enough
 // that the partial sums stay small.
-constexpr int64_t MAX_PARTS = 256;
 int col_parts(int64_t rows) { return static_cast<int>(rows < MAX_PARTS ? (rows > 0 ? rows : 1) : MAX_PARTS); }
 
 // ---------------------------------------------------------------- products
@@ -296,7 +295,8 @@ qta_status qta_norm(const qta_norm_desc* d, const qta_mat* x, const qta_mat* res
 size_t qta_norm_bwd_workspace_bytes(const qta_norm_desc* d)
 {
     if (check_norm_desc(d) != QTA_OK) return 0;
-    return static_cast<size_t>(col_parts(d->rows)) * 2 * d->cols * sizeof(float);
+    const int64_t parts = col_parts(d->rows);   // the row kernels use at least 8
+    return static_cast<size_t>(parts < 8 ? 8 : parts) * 2 * d->cols * sizeof(float);
 }
 
 qta_status qta_norm_bwd(const qta_norm_desc* d, const qta_mat* dy, const qta_mat* s, const void* gamma,

@@ -1,5 +1,5 @@
 // qta_norm.cu -- norm kernels and launchers of the layer operators.
-#include "qta_layer.cuh"
+#include "qta_norm_rows.cuh"
 
 namespace qta {
 
@@ -121,39 +121,113 @@ __global__ void __launch_bounds__(256) col_sum_kernel(const void* a, int64_t ld,
 }
 
 // out0[c] = sum over i < parts of part[i * stride + c], out1 the same one
-// block of `cols` further: the partial sums in a fixed order.
-__global__ void __launch_bounds__(256) col_finish_kernel(const float* part, int64_t stride, int parts, int64_t cols,
-                                                         float* out0, float* out1)
+// block of `cols` further: the partial sums in a fixed order (warp w of 16
+// adds the rows w, w + 16, ..., then the warps in turn).
+constexpr int FINISH_WARPS = 16;
+__global__ void __launch_bounds__(32 * FINISH_WARPS) col_finish_kernel(const float* part, int64_t stride, int parts,
+                                                                       int64_t cols, float* out0, float* out1)
 {
+    __shared__ float sums[FINISH_WARPS][32];
     pdl_wait();
     pdl_trigger();
-    const int64_t c = blockIdx.x * 256LL + threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = blockIdx.x * 32LL + lane;
     float* out = blockIdx.y ? out1 : out0;
-    if (c >= cols || !out) return;
     const float* p = part + blockIdx.y * cols + c;
     float s = 0.0f;
-    for (int i = 0; i < parts; ++i) s += p[i * stride];
-    out[c] = s;
+    if (c < cols && out) {
+#pragma unroll 4
+        for (int i = warp; i < parts; i += FINISH_WARPS) s += p[i * stride];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < cols && out) {
+#pragma unroll
+        for (int w = 1; w < FINISH_WARPS; ++w) s += sums[w][lane];
+        out[c] = s;
+    }
 }
 
-cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream)
+cudaError_t launch_norm_rows_bf16(const NormParams&, const RowPlan&, int, cudaStream_t);
+cudaError_t launch_norm_rows_fp16(const NormParams&, const RowPlan&, int, cudaStream_t);
+cudaError_t launch_norm_rows_fp32(const NormParams&, const RowPlan&, int, cudaStream_t);
+cudaError_t launch_norm_bwd_rows_bf16(const NormBwdParams&, const RowPlan&, cudaStream_t);
+cudaError_t launch_norm_bwd_rows_fp16(const NormBwdParams&, const RowPlan&, cudaStream_t);
+cudaError_t launch_norm_bwd_rows_fp32(const NormBwdParams&, const RowPlan&, cudaStream_t);
+
+// Whether the row kernels take matrices whose rows start at these addresses
+// (n of them, NULL: absent), and the vectors of a row.
+static bool row_form(const void* const* base, const int64_t* ld, int n, int64_t cols, int dt, int max_threads,
+                     int* shift, int* aligned, RowPlan* q)
 {
+    const int es = dt_size(dt), N = 16 / es;
+    bool all = true;
+    *shift = static_cast<int>((reinterpret_cast<uintptr_t>(base[0]) / es) % N);
+    for (int i = 0; i < n; ++i) {
+        if (!base[i]) continue;
+        if (static_cast<int>((reinterpret_cast<uintptr_t>(base[i]) / es) % N) != *shift || (ld[i] - ld[0]) % N)
+            return false;
+        all = all && ld[i] % N == 0;
+    }
+    *aligned = all && *shift == 0 && cols % N == 0;
+    if (cols > (1 << 20)) return false;
+    return row_plan(*aligned ? cols / N : (cols + N - 1) / N + 1, max_threads, q);
+}
+
+static bool vec16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+cudaError_t launch_norm(const NormParams& in, int sms, cudaStream_t stream)
+{
+    NormParams p = in;
+    p.w_vec = vec16(p.gamma) && vec16(p.beta);
+    const void* base[4] = {p.x, p.residual, p.y, p.sum};
+    const int64_t ld[4] = {p.ld_x, p.ld_r, p.ld_y, p.ld_s};
+    RowPlan q;
+    if (row_form(base, ld, 4, p.cols, p.dt, p.rows > sms ? 256 : 32, &p.shift, &p.aligned, &q)) {
+        if (p.dt == 0) return launch_norm_rows_bf16(p, q, sms, stream);
+        if (p.dt == 1) return launch_norm_rows_fp16(p, q, sms, stream);
+        return launch_norm_rows_fp32(p, q, sms, stream);
+    }
     const int64_t most = 16LL * sms;
     return launch_pdl(norm_rows_kernel, dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)), dim3(ROW_THREADS),
                       0, stream, p);
 }
 
-cudaError_t launch_norm_bwd(const NormBwdParams& p, int sms, cudaStream_t stream)
+cudaError_t launch_norm_bwd(const NormBwdParams& in, int sms, cudaStream_t stream)
 {
+    NormBwdParams p = in;
+    p.w_vec = vec16(p.gamma);
+    const void* base[4] = {p.s, p.dy, p.dsum, p.dx};
+    const int64_t ld[4] = {p.ld_s, p.ld_dy, p.ld_ds, p.ld_dx};
+    RowPlan q;
+    cudaError_t e;
+    const unsigned nf = static_cast<unsigned>((p.cols + 31) / 32);
+    if (row_form(base, ld, 4, p.cols, p.dt, p.rows > sms ? BWD_MAX_THREADS : 32, &p.shift, &p.aligned, &q)) {
+        // CTAs: what fits on the GPU, or the rows; a multiple of 8 where the rows' shifts differ
+        int64_t parts = (p.rows + q.G - 1) / q.G;
+        if (parts > sms) parts = sms;
+        if (parts > MAX_PARTS) parts = MAX_PARTS;
+        if (!p.aligned) parts = parts < 8 ? 8 : parts / 8 * 8;
+        p.parts = static_cast<int>(parts);
+        if (p.dt == 0)
+            e = launch_norm_bwd_rows_bf16(p, q, stream);
+        else if (p.dt == 1)
+            e = launch_norm_bwd_rows_fp16(p, q, stream);
+        else
+            e = launch_norm_bwd_rows_fp32(p, q, stream);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(col_finish_kernel, dim3(nf, p.dbeta ? 2 : 1), dim3(32 * FINISH_WARPS), 0, stream,
+                          static_cast<const float*>(p.part), 2 * p.cols, p.parts, p.cols, p.dgamma, p.dbeta);
+    }
     const int64_t most = 16LL * sms;
     const unsigned nc = static_cast<unsigned>((p.cols + 255) / 256);
-    cudaError_t e = launch_pdl(norm_bwd_rows_kernel, dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)),
+    e = launch_pdl(norm_bwd_rows_kernel, dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)),
                                dim3(ROW_THREADS), 0, stream, p);
     if (e != cudaSuccess) return e;
     e = launch_pdl(norm_bwd_cols_kernel, dim3(nc, p.parts), dim3(256), 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(col_finish_kernel, dim3(nc, 2), dim3(256), 0, stream, static_cast<const float*>(p.part),
-                      2 * p.cols, p.parts, p.cols, p.dgamma, p.dbeta);
+    return launch_pdl(col_finish_kernel, dim3(nf, 2), dim3(32 * FINISH_WARPS), 0, stream,
+                      static_cast<const float*>(p.part), 2 * p.cols, p.parts, p.cols, p.dgamma, p.dbeta);
 }
 
 cudaError_t launch_col_sum(const void* a, int64_t ld, int dt, int64_t rows, int64_t cols, int parts, float* part,
@@ -166,8 +240,8 @@ cudaError_t launch_col_sum(const void* a, int64_t ld, int dt, int64_t rows, int6
 cudaError_t launch_col_finish(const float* part, int64_t stride, int parts, int64_t cols, float* out,
                               cudaStream_t stream)
 {
-    return launch_pdl(col_finish_kernel, dim3(static_cast<unsigned>((cols + 255) / 256), 1), dim3(256), 0, stream,
-                      part, stride, parts, cols, out, static_cast<float*>(nullptr));
+    return launch_pdl(col_finish_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1), dim3(32 * FINISH_WARPS), 0,
+                      stream, part, stride, parts, cols, out, static_cast<float*>(nullptr));
 }
 
 }  // namespace qta

@@ -19,6 +19,8 @@ struct NormParams {
     int64_t ld_x, ld_r, ld_y, ld_s;
     float eps;
     int dt, w_dt, rms;
+    int shift;              // elements from a 16-byte boundary to row 0
+    int aligned, w_vec;     // rows are whole aligned vectors; gamma and beta are 16-byte aligned
 };
 
 struct NormBwdParams {
@@ -36,6 +38,7 @@ struct NormBwdParams {
     int64_t ld_dy, ld_s, ld_ds, ld_dx;
     int parts;
     int dt, w_dt, rms;
+    int shift, aligned, w_vec;   // as above
 };
 
 }  // namespace qta

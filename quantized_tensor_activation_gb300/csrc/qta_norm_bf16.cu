@@ -1,0 +1,16 @@
+// qta_norm_bf16.cu -- the row kernels of the norms for bf16 activations.
+#include "qta_norm_rows.cuh"
+
+namespace qta {
+
+cudaError_t launch_norm_rows_bf16(const NormParams& p, const RowPlan& q, int sms, cudaStream_t stream)
+{
+    return pick_row_kernel<0>(p, q, RunFwd{p, q, sms, stream});
+}
+
+cudaError_t launch_norm_bwd_rows_bf16(const NormBwdParams& p, const RowPlan& q, cudaStream_t stream)
+{
+    return pick_row_kernel<0>(p, q, RunBwd{p, q, stream});
+}
+
+}  // namespace qta

@@ -1,0 +1,16 @@
+// qta_norm_fp16.cu -- the row kernels of the norms for fp16 activations.
+#include "qta_norm_rows.cuh"
+
+namespace qta {
+
+cudaError_t launch_norm_rows_fp16(const NormParams& p, const RowPlan& q, int sms, cudaStream_t stream)
+{
+    return pick_row_kernel<1>(p, q, RunFwd{p, q, sms, stream});
+}
+
+cudaError_t launch_norm_bwd_rows_fp16(const NormBwdParams& p, const RowPlan& q, cudaStream_t stream)
+{
+    return pick_row_kernel<1>(p, q, RunBwd{p, q, stream});
+}
+
+}  // namespace qta
