@@ -29,4 +29,24 @@ struct GemmTile {
 GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int groups, int sms);
 cudaError_t launch_gemm(int form, int epi, const GemmTile& t, const GemmParams& p, int sms, cudaStream_t stream);
 
+// Products of up to SKINNY_ROWS tokens (qta_skinny.cu).
+constexpr int64_t SKINNY_ROWS = 16;
+
+struct SkinnyParams {
+    const uint8_t* x;
+    int64_t ldx;
+    const uint8_t* w[2];    // the weight, or the gate's and the up projection's
+    int64_t ldw[2];
+    int M, N, K;
+    int act;
+    const void* bias;
+    int bias_dt;
+    const void* aux;        // residual of type out_dt (NULL: none)
+    int64_t ld_aux;
+    void* out;
+    int64_t ld_out;
+    int out_dt;
+};
+cudaError_t launch_skinny(int dt, bool dual, const SkinnyParams& p, cudaStream_t stream);
+
 }  // namespace qta

@@ -216,6 +216,36 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
     return cuda_status(launch_gemm(form, epi, t, p, sms, s));
 }
 
+// The same for few rows.
+qta_status run_skinny(int32_t dt, const View& x, const View& w0, const View* w1, const void* bias, int32_t bias_dt,
+                      const View* aux, const View& out, int32_t out_dt, int32_t act, cudaStream_t s)
+{
+    SkinnyParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = static_cast<const uint8_t*>(x.p);
+    p.ldx = x.ld;
+    p.w[0] = static_cast<const uint8_t*>(w0.p);
+    p.ldw[0] = w0.ld;
+    if (w1) {
+        p.w[1] = static_cast<const uint8_t*>(w1->p);
+        p.ldw[1] = w1->ld;
+    }
+    p.M = static_cast<int>(x.rows);
+    p.N = static_cast<int>(w0.rows);
+    p.K = static_cast<int>(x.cols);
+    p.act = act;
+    p.bias = bias;
+    p.bias_dt = bias_dt;
+    if (aux) {
+        p.aux = aux->p;
+        p.ld_aux = aux->ld;
+    }
+    p.out = out.w();
+    p.ld_out = out.ld;
+    p.out_dt = out_dt;
+    return cuda_status(launch_skinny(dt, w1 != nullptr, p, s));
+}
+
 GemmParams blank()
 {
     GemmParams p;
@@ -377,6 +407,9 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     o.output(vy);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
+    if (d->rows <= SKINNY_ROWS)
+        return run_skinny(d->dtype, vx, vw, nullptr, bias, d->bias_dtype, residual ? &vr : nullptr, vy, d->out_dtype,
+                          d->act, reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();
     p.act = d->act;
     p.bias = bias;
@@ -482,6 +515,9 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     o.output(vh);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
+    if (d->rows <= SKINNY_ROWS)
+        return run_skinny(d->dtype, vx, vg, &vu, nullptr, 0, nullptr, vh, d->dtype, d->act,
+                          reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();
     p.act = d->act;
     p.out_dt = d->dtype;

@@ -1,0 +1,181 @@
+// qta_skinny.cu -- products of few tokens: y = f(x w^T + b) + r and the gated
+// block for up to 16 rows of x, where reading the weights once is all that
+// counts (2 M operations per 2-byte weight: HBM-bound up to M of several
+// hundred, while a tcgen05 tile would be 7/8 empty and its ring one CTA deep).
+//
+// A CTA owns 16 output channels (of both weights in the gated form); its 8
+// warps split the contraction in steps of 32, interleaved, so that a CTA reads
+// 512 consecutive bytes of each weight row at a time.  Every lane loads 16
+// consecutive bytes of a weight row straight into the registers that
+// mma.sync.m16n8k16 takes: the contraction order inside a product is free, so
+// lane t of a quad takes elements 8t .. 8t+7 of a step as its share of two
+// products, in A and B alike, and nothing passes through shared memory.  The
+// warps' sums are added in warp order.
+#include "qta_layer.cuh"
+
+namespace qta {
+
+constexpr int SK_WARPS = 8;
+constexpr int SK_ROWS = 16;
+constexpr int SK_STEP = 32;
+
+// 16 bytes where `on`, else zeros: a predicated load, so that a batch of them
+// is issued without a branch between.  Weights pass L1 by.
+template <bool WEIGHT>
+__device__ __forceinline__ uint4 ld_if(const uint8_t* p, bool on)
+{
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (WEIGHT)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+            : "l"(p), "r"(on ? 1u : 0u));
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)
+            : "l"(p), "r"(on ? 1u : 0u));
+    return w;
+}
+
+// Zeros from element n on (what lies past a row's end is not the matrix's and
+// may be anything).
+__device__ __forceinline__ void clip8(uint4& w, int n)
+{
+    uint32_t* v = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 2 * i >= n ? 0u : 2 * i + 1 >= n ? v[i] & 0xffffu : v[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    if constexpr (DT == 0)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: tokens in groups of 8.  DUAL: the gated form.
+template <int DT, int NT, bool DUAL>
+__global__ void __launch_bounds__(32 * SK_WARPS, NT == 1 ? 3 : 2) skinny_kernel(const SkinnyParams p)
+{
+    constexpr int W = DUAL ? 2 : 1;
+    constexpr int U = DUAL ? 2 : 4;   // steps whose loads are in flight together
+    __shared__ float part[SK_WARPS][W][8 * NT][SK_ROWS + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = blockIdx.x * SK_ROWS;
+    pdl_wait();
+    pdl_trigger();
+
+    // rows past N repeat the last one; their sums are not stored
+    const int ra = min(n0 + g, p.N - 1), rb = min(n0 + g + 8, p.N - 1);
+    const uint8_t* wa[W];
+    const uint8_t* wb[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        wa[i] = p.w[i] + 2 * p.ldw[i] * ra;
+        wb[i] = p.w[i] + 2 * p.ldw[i] * rb;
+    }
+    const uint8_t* xr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xr[j] = p.x + 2 * p.ldx * min(8 * j + g, p.M - 1);
+    float c[W][NT][4];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[i][j][e] = 0.0f;
+
+    const int steps = (p.K + SK_STEP - 1) / SK_STEP;
+    for (int s = warp; s < steps; s += SK_WARPS * U) {
+        uint4 a[U][W], b[U][W], x[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (s + u * SK_WARPS) * SK_STEP + 8 * t;   // past the last step: k >= K, zeros
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                a[u][i] = ld_if<true>(wa[i] + 2LL * k, k < p.K);
+                b[u][i] = ld_if<true>(wb[i] + 2LL * k, k < p.K);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[u][j] = ld_if<false>(xr[j] + 2LL * k, k < p.K && 8 * j + g < p.M);
+        }
+        if (p.K & 7) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int n = p.K - (s + u * SK_WARPS) * SK_STEP - 8 * t;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    clip8(a[u][i], n);
+                    clip8(b[u][i], n);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) clip8(x[u][j], n);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    mma16816<DT>(c[i][j], a[u][i].x, b[u][i].x, a[u][i].y, b[u][i].y, x[u][j].x, x[u][j].y);
+                    mma16816<DT>(c[i][j], a[u][i].z, b[u][i].z, a[u][i].w, b[u][i].w, x[u][j].z, x[u][j].w);
+                }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            part[warp][i][8 * j + 2 * t][g] = c[i][j][0];
+            part[warp][i][8 * j + 2 * t + 1][g] = c[i][j][1];
+            part[warp][i][8 * j + 2 * t][g + 8] = c[i][j][2];
+            part[warp][i][8 * j + 2 * t + 1][g + 8] = c[i][j][3];
+        }
+    __syncthreads();
+    const int e = threadIdx.x, row = e & (SK_ROWS - 1), m = e / SK_ROWS, n = n0 + row;   // 256 threads: 16 x 16
+    if (m >= p.M || n >= p.N) return;
+    float v[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        v[i] = part[0][i][m][row];
+#pragma unroll
+        for (int w = 1; w < SK_WARPS; ++w) v[i] += part[w][i][m][row];
+    }
+    if (p.bias) v[0] += load_elem(p.bias, n, p.bias_dt);
+    with_act(p.act, [&](auto tag) { v[0] = act_value<decltype(tag)::value>(v[0]); });
+    if constexpr (DUAL) v[0] *= v[1];
+    if (p.aux) v[0] += load_elem(p.aux, m * p.ld_aux + n, p.out_dt);
+    store_elem(p.out, m * p.ld_out + n, p.out_dt, v[0]);
+}
+
+template <int DT>
+static cudaError_t launch_s(bool dual, const SkinnyParams& p, cudaStream_t stream)
+{
+    const dim3 grid((p.N + SK_ROWS - 1) / SK_ROWS), block(32 * SK_WARPS);
+    if (dual)
+        return p.M <= 8 ? launch_pdl(skinny_kernel<DT, 1, true>, grid, block, 0, stream, p)
+                        : launch_pdl(skinny_kernel<DT, 2, true>, grid, block, 0, stream, p);
+    return p.M <= 8 ? launch_pdl(skinny_kernel<DT, 1, false>, grid, block, 0, stream, p)
+                    : launch_pdl(skinny_kernel<DT, 2, false>, grid, block, 0, stream, p);
+}
+
+cudaError_t launch_skinny(int dt, bool dual, const SkinnyParams& p, cudaStream_t stream)
+{
+    return dt == 0 ? launch_s<0>(dual, p, stream) : launch_s<1>(dual, p, stream);
+}
+
+}  // namespace qta

@@ -20,7 +20,8 @@ import ctypes
 
 import torch
 
-from . import BF16, FP16, FP32, _check, _stream, lib
+from . import BF16, FP16, FP32, _check, lib
+from . import _stream as _given_stream
 
 NORM_LAYER, NORM_RMS = 0, 1
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF = range(5)
@@ -151,6 +152,12 @@ def _vec(name, t, n, dt):
     return t.data_ptr()
 
 
+def _stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device (the raw query: a tenth of the time of
+    torch.cuda.current_stream())."""
+    return _given_stream(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _work(t, need):
     if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < need:
         raise ValueError(f"ws: a contiguous CUDA buffer of at least {need} bytes is needed")
@@ -165,7 +172,7 @@ def qta_norm(d: NormDesc, x, gamma, y, beta=None, residual=None, sum_out=None, m
     _check("qta_norm", _lib().qta_norm(
         d, _mat("x", x, R, C, dt), _mat("residual", residual, R, C, dt), _vec("gamma", gamma, C, d.w_dtype),
         _vec("beta", beta, C, d.w_dtype), _mat("y", y, R, C, dt), _mat("sum_out", sum_out, R, C, dt),
-        _vec("mean", mean, R, FP32), _vec("rstd", rstd, R, FP32), _stream(stream)))
+        _vec("mean", mean, R, FP32), _vec("rstd", rstd, R, FP32), _stream(stream, x)))
 
 
 def qta_norm_bwd(d: NormDesc, dy, s, gamma, rstd, dx, dgamma, ws, mean=None, dbeta=None, dsum=None,
@@ -176,7 +183,7 @@ def qta_norm_bwd(d: NormDesc, dy, s, gamma, rstd, dx, dgamma, ws, mean=None, dbe
         d, _mat("dy", dy, R, C, dt), _mat("s", s, R, C, dt), _vec("gamma", gamma, C, d.w_dtype),
         _vec("mean", mean, R, FP32), _vec("rstd", rstd, R, FP32), _mat("dsum", dsum, R, C, dt),
         _mat("dx", dx, R, C, dt), _vec("dgamma", dgamma, C, FP32), _vec("dbeta", dbeta, C, FP32),
-        _work(ws, norm_bwd_workspace_bytes(d)), _stream(stream)))
+        _work(ws, norm_bwd_workspace_bytes(d)), _stream(stream, dy)))
 
 
 def qta_linear(d: LinearDesc, x, w, y, bias=None, residual=None, stream=None) -> None:
@@ -184,7 +191,7 @@ def qta_linear(d: LinearDesc, x, w, y, bias=None, residual=None, stream=None) ->
     R, N, K = d.rows, d.n_out, d.n_in
     _check("qta_linear", _lib().qta_linear(
         d, _mat("x", x, R, K, d.dtype), _mat("w", w, N, K, d.dtype), _vec("bias", bias, N, d.bias_dtype),
-        _mat("residual", residual, R, N, d.out_dtype), _mat("y", y, R, N, d.out_dtype), _stream(stream)))
+        _mat("residual", residual, R, N, d.out_dtype), _mat("y", y, R, N, d.out_dtype), _stream(stream, x)))
 
 
 def qta_linear_bwd(d: LinearDesc, dy, x, w, dx, dw, ws, bias=None, dbias=None, stream=None) -> None:
@@ -193,7 +200,7 @@ def qta_linear_bwd(d: LinearDesc, dy, x, w, dx, dw, ws, bias=None, dbias=None, s
     _check("qta_linear_bwd", _lib().qta_linear_bwd(
         d, _mat("dy", dy, R, N, d.dtype), _mat("x", x, R, K, d.dtype), _mat("w", w, N, K, d.dtype),
         _vec("bias", bias, N, d.bias_dtype), _mat("dx", dx, R, K, d.dtype), _mat("dw", dw, N, K, d.grad_dtype),
-        _vec("dbias", dbias, N, FP32), _work(ws, linear_bwd_workspace_bytes(d)), _stream(stream)))
+        _vec("dbias", dbias, N, FP32), _work(ws, linear_bwd_workspace_bytes(d)), _stream(stream, dy)))
 
 
 def qta_gated_ffn(d: FfnDesc, x, wg, wu, h, stream=None) -> None:
@@ -201,7 +208,7 @@ def qta_gated_ffn(d: FfnDesc, x, wg, wu, h, stream=None) -> None:
     R, H, F, dt = d.rows, d.hidden, d.width, d.dtype
     _check("qta_gated_ffn", _lib().qta_gated_ffn(
         d, _mat("x", x, R, H, dt), _mat("wg", wg, F, H, dt), _mat("wu", wu, F, H, dt), _mat("h", h, R, F, dt),
-        _stream(stream)))
+        _stream(stream, x)))
 
 
 def qta_gated_ffn_bwd(d: FfnDesc, dh, x, wg, wu, dx, dwg, dwu, ws, stream=None) -> None:
@@ -210,4 +217,4 @@ def qta_gated_ffn_bwd(d: FfnDesc, dh, x, wg, wu, dx, dwg, dwu, ws, stream=None) 
     _check("qta_gated_ffn_bwd", _lib().qta_gated_ffn_bwd(
         d, _mat("dh", dh, R, F, dt), _mat("x", x, R, H, dt), _mat("wg", wg, F, H, dt), _mat("wu", wu, F, H, dt),
         _mat("dx", dx, R, H, dt), _mat("dwg", dwg, F, H, d.grad_dtype), _mat("dwu", dwu, F, H, d.grad_dtype),
-        _work(ws, gated_ffn_bwd_workspace_bytes(d)), _stream(stream)))
+        _work(ws, gated_ffn_bwd_workspace_bytes(d)), _stream(stream, dh)))
