@@ -3,71 +3,91 @@
 
 namespace qta {
 
-// Tiles of a launch.
-struct Plan {
-    int cg, bn;
-};
+// Pairs where more than half of them find a 256 x 256 tile, else the split
+// kernel: its 128 x 128 tiles, at most as many as SMs, with the contraction of
+// each split until the GPU is full (2, 4 or 8 CTAs; each keeps at least
+// MIN_SPLIT_BLOCKS blocks, below which the join costs more than the split
+// gains).
+constexpr int MIN_SPLIT_BLOCKS = 3;
 
-static Plan plan_of(int form, int epi, int64_t M, int64_t N, int groups, int sms)
+GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms)
 {
+    (void)form;
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const int64_t pairs = ((M + 255) / 256) * ((N + (dual ? 127 : 255)) / (dual ? 128 : 256)) * groups;
-    if (pairs >= sms / 2) return {2, 256};
-    return {1, 128};
-}
-
-GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int groups, int sms)
-{
-    const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const Plan q = plan_of(form, epi, M, N, groups, sms);
-    return {q.cg * GEMM_BM, dual ? q.bn / 2 : q.bn, dual ? 128 * q.bn / 256 : q.bn / q.cg, q.cg, q.bn};
-}
-
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
-static cudaError_t launch_g(const GemmParams& p, int sms, cudaStream_t stream)
-{
-    using C = GemmCfg<CG, BN>;
-    static std::atomic<unsigned> done{0};
-    auto fn = gemm_kernel<CG, BN, A_MN, B_MN, EPI>;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), C::SMEM, &done);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.groups;
-    int64_t slots = sms;
-    if constexpr (CG == 2) {   // pairs that can be resident at once (an odd SM of a cluster of SMs has no partner)
-        static std::atomic<int> pairs{0};
-        int n = pairs.load();
-        if (n == 0) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
-            cfg.blockDim = dim3(GEMM_THREADS);
-            cfg.dynamicSmemBytes = C::SMEM;
-            if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = sms / 2;
-            pairs.store(n);
-        }
-        slots = n;
-    }
-    GemmParams q = p;
-    q.idesc |= idesc_f16(GEMM_BM * CG, BN, false, A_MN, B_MN);
-    return launch_pdl(fn, dim3(static_cast<unsigned>((tiles < slots ? tiles : slots) * CG)), dim3(GEMM_THREADS),
-                      C::SMEM, stream, q);
+    const int64_t pair_n = dual ? 128 : 256, pairs = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n) * groups;
+    const int64_t tile_n = dual ? 64 : 128, tiles = ((M + 127) / 128) * ((N + tile_n - 1) / tile_n) * groups;
+    if (tiles > sms) return {256, static_cast<int>(pair_n), 128, 0};
+    (void)pairs;
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= sms && blocks >= 2 * s * MIN_SPLIT_BLOCKS) s *= 2;
+    return {128, static_cast<int>(tile_n), static_cast<int>(tile_n), s};
 }
 
 template <bool A_MN, bool B_MN, int EPI>
-static cudaError_t launch_t(const GemmTile& t, const GemmParams& p, int sms, cudaStream_t stream)
+static cudaError_t launch_pairs(const GemmParams& p, int sms, cudaStream_t stream)
 {
-    if (t.cg == 2) return launch_g<2, 256, A_MN, B_MN, EPI>(p, sms, stream);
-    return launch_g<1, 128, A_MN, B_MN, EPI>(p, sms, stream);
+    static std::atomic<unsigned> done{0};
+    auto fn = gemm_kernel<A_MN, B_MN, EPI>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), GEMM_SMEM, &done);
+    if (e != cudaSuccess) return e;
+    // pairs that can be resident at once (an odd SM of a cluster of SMs has no partner)
+    static std::atomic<int> slots{0};
+    int n = slots.load();
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+        cfg.blockDim = dim3(GEMM_THREADS);
+        cfg.dynamicSmemBytes = GEMM_SMEM;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = sms / 2;
+        slots.store(n);
+    }
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.groups;
+    GemmParams q = p;
+    q.idesc |= idesc_f16(2 * GEMM_BM, 256, false, A_MN, B_MN);
+    return launch_pdl(fn, dim3(static_cast<unsigned>((tiles < n ? tiles : n) * 2)), dim3(GEMM_THREADS), GEMM_SMEM,
+                      stream, q);
 }
 
-cudaError_t launch_gemm(int form, int epi, const GemmTile& t, const GemmParams& p, int sms, cudaStream_t stream)
+template <bool A_MN, bool B_MN, int EPI>
+static cudaError_t launch_split(const GemmParams& p, cudaStream_t stream)
 {
-    if (form == FORM_NN) return launch_t<false, true, EPI_LINEAR>(t, p, sms, stream);
-    if (form == FORM_TN) return launch_t<true, true, EPI_LINEAR>(t, p, sms, stream);
+    static std::atomic<unsigned> done{0};
+    auto fn = gemm_split_kernel<A_MN, B_MN, EPI>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), SPLIT_SMEM, &done);
+    if (e != cudaSuccess) return e;
+    GemmParams q = p;
+    q.idesc |= idesc_f16(GEMM_BM, 128, false, A_MN, B_MN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_m * p.tiles_n * p.groups * p.split));
+    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.dynamicSmemBytes = SPLIT_SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fn, q);
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+static cudaError_t launch_t(const GemmParams& p, int sms, cudaStream_t stream)
+{
+    return p.split ? launch_split<A_MN, B_MN, EPI>(p, stream) : launch_pairs<A_MN, B_MN, EPI>(p, sms, stream);
+}
+
+cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream)
+{
+    if (form == FORM_NN) return launch_t<false, true, EPI_LINEAR>(p, sms, stream);
+    if (form == FORM_TN) return launch_t<true, true, EPI_LINEAR>(p, sms, stream);
     switch (epi) {
-    case EPI_LINEAR: return launch_t<false, false, EPI_LINEAR>(t, p, sms, stream);
-    case EPI_LINEAR_BWD: return launch_t<false, false, EPI_LINEAR_BWD>(t, p, sms, stream);
-    case EPI_GATED: return launch_t<false, false, EPI_GATED>(t, p, sms, stream);
-    case EPI_GATED_BWD: return launch_t<false, false, EPI_GATED_BWD>(t, p, sms, stream);
+    case EPI_LINEAR: return launch_t<false, false, EPI_LINEAR>(p, sms, stream);
+    case EPI_LINEAR_BWD: return launch_t<false, false, EPI_LINEAR_BWD>(p, sms, stream);
+    case EPI_GATED: return launch_t<false, false, EPI_GATED>(p, sms, stream);
+    case EPI_GATED_BWD: return launch_t<false, false, EPI_GATED_BWD>(p, sms, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -3,13 +3,14 @@
 //   D[m, n] = sum_k A[m, k] B[n, k]   (FP32 accumulators in TMEM)
 //
 // with an epilogue that finishes the operator in registers.  A pair of CTAs
-// (or one CTA) computes tiles of 256 (128) x BN: warp 0 loads A and B in blocks
-// of 64 contraction elements by TMA into a ring of shared-memory stages, warp
+// computes tiles of 256 x 256: warp 0 loads A and B in blocks of 64
+// contraction elements by TMA into a ring of shared-memory stages, warp
 // 1 issues tcgen05.mma on them, warps 2-9 read the accumulators of the
 // previous tile (TMEM holds two) and run the epilogue.  In a pair each CTA
 // loads and keeps half of B, so a byte of shared memory feeds twice the
-// products that it feeds in a single CTA: the single CTA's 128 x 128 tile is
-// bound by shared memory.  Operands whose contraction index is
+// products that it feeds in a single CTA, whose 128 x 128 tile is bound by
+// shared memory (8192 x 8192 -> 3584 gated, fp16: 1004 us in single CTAs, 644
+// in pairs).  Products too small for the pairs run the split kernel below.  Operands whose contraction index is
 // not the contiguous one (the backward products) are read as they lie, with
 // MN-major descriptors: nothing is transposed in memory.
 //
@@ -52,34 +53,29 @@ struct GemmParams {
     // boxes of 32 rows x epi_box_cols; else by per-thread loads and stores
     int staged;
     CUtensorMap aux_map, out_map[2];
+    int split;                  // CTAs that share a tile's contraction (split kernel)
     unsigned int* err;
 };
 
 constexpr int GEMM_BM = 128;   // rows of one CTA's share of a tile
 constexpr int GEMM_BK = 64;
+constexpr int GEMM_STAGES = 6;
 constexpr int GEMM_EPI_WARPS = 8;
 constexpr int GEMM_THREADS = 64 + 32 * GEMM_EPI_WARPS;
 constexpr int EPI_BUF = 4096;   // staging bytes of an epilogue warp: 32 rows x 128 bytes
 
-// CG CTAs compute one tile of CG * 128 x BN; each holds its 128 rows of A and
-// its BN / CG rows of B.
-template <int CG, int BN>
-struct GemmCfg {
-    static constexpr int BN_CTA = BN / CG;
-    static constexpr int A_BYTES = GEMM_BM * GEMM_BK * 2;
-    static constexpr int B_BYTES = BN_CTA * GEMM_BK * 2;
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 6;
-    static constexpr int SMEM = STAGES * STAGE + GEMM_EPI_WARPS * EPI_BUF + 1024;   // + slack to start on 1024 bytes
-    static constexpr uint32_t TMEM_COLS = 2 * BN;        // two accumulators
-};
+// A stage holds 128 rows of A and 128 of B: the pair's tile is 256 x 256, each
+// CTA with its half of both; the split kernel's 128 x 128.
+constexpr int GEMM_A_BYTES = GEMM_BM * GEMM_BK * 2;
+constexpr int GEMM_STAGE = 2 * GEMM_A_BYTES;
+constexpr int GEMM_SMEM = GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * EPI_BUF + 1024;   // + slack to start on 1024 bytes
+constexpr int SPLIT_SMEM = GEMM_STAGES * GEMM_STAGE + 1024;
 
 // Columns that an epilogue warp stages at a time: rows of 128 bytes, or of 64
-// where its buffer holds two outputs or its share of the tile is 32 columns.
-__host__ __device__ constexpr int epi_box_cols(int epi, int bn, bool fp32)
+// where its buffer holds two outputs.
+__host__ __device__ constexpr int epi_box_cols(int epi, bool fp32)
 {
-    const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    return fp32 || epi == EPI_GATED_BWD || (dual ? bn / 4 : bn / 2) < 64 ? 32 : 64;
+    return fp32 || epi == EPI_GATED_BWD ? 32 : 64;
 }
 
 // Tiles in an order that keeps a wave of CTAs on few rows and columns of
@@ -197,42 +193,88 @@ __device__ __forceinline__ float column_sum32(float (&v)[32], int lane)
     return v[0];
 }
 
-template <int CG, int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p)
+// The operator on 32 columns of a row: v (and u, the up projection's) hold the
+// accumulators, x aux where there is one; v (and u) leave as the outputs.
+template <int EPI, int NU>
+__device__ __forceinline__ void piece_math(const GemmParams& p, int col, int n, bool live, const float (&x)[32],
+                                           float (&v)[32], float (&u)[NU])
 {
-    using C = GemmCfg<CG, BN>;
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
-    constexpr int TILE_N = DUAL ? BN / 2 : BN;   // output columns of a tile
+    if constexpr (!DUAL) {
+        if (p.bias) {
+            float b[32];
+            row_load32(p.bias, col, p.bias_dt, n, b);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += b[i];
+        }
+    }
+    with_act(p.act, [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if constexpr (EPI == EPI_LINEAR) {
+                v[i] = act_value<ACT>(v[i]);
+            } else if constexpr (EPI == EPI_GATED) {
+                v[i] = act_value<ACT>(v[i]) * u[i];
+            } else {
+                float f, df;
+                act_both<ACT>(v[i], f, df);
+                if constexpr (EPI == EPI_LINEAR_BWD) {
+                    v[i] = live && i < n ? x[i] * df : 0.0f;
+                } else {
+                    v[i] = x[i] * u[i] * df;
+                    u[i] = x[i] * f;
+                }
+            }
+        }
+    });
+    if constexpr (EPI == EPI_LINEAR) {
+        if (p.aux) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += x[i];
+        }
+    }
+}
+
+// Column sums of dz over the 32 rows from row0 on.
+__device__ __forceinline__ void piece_colsum(const GemmParams& p, int row0, int col, int n, int lane, float (&v)[32])
+{
+    const float sum = column_sum32(v, lane);
+    if (lane < n) p.colsum[static_cast<int64_t>(row0 / 32) * p.N + col + lane] = sum;
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+    constexpr int BN = 256, TILE_N = DUAL ? BN / 2 : BN;   // accumulator and output columns of a tile
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[GEMM_STAGES], empty[GEMM_STAGES], acc_full[2], acc_empty[2], drain;
     __shared__ uint64_t aux_full[GEMM_EPI_WARPS];
     __shared__ uint32_t tmem_slot;
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int rank = static_cast<int>(cluster_rank());
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
+        for (int i = 0; i < GEMM_STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], GEMM_EPI_WARPS * CG);
+            mbar_init(&acc_empty[i], GEMM_EPI_WARPS * 2);
         }
         for (int i = 0; i < GEMM_EPI_WARPS; ++i) mbar_init(&aux_full[i], 1);
         mbar_init(&drain, 1);
         fence_barrier_init();
     }
     __syncwarp();
-    if (warp == 1) tmem_alloc<CG>(&tmem_slot, C::TMEM_COLS);
+    if (warp == 1) tmem_alloc<2>(&tmem_slot, 2 * BN);
     tc_fence_before();
-    if constexpr (CG == 2)
-        cluster_sync();   // the barriers of both CTAs exist before either signals the other
-    else
-        __syncthreads();
+    cluster_sync();   // the barriers of both CTAs exist before either signals the other
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
@@ -250,8 +292,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                 const int g = t / per_group, r = t - g * per_group;
                 int tm, tn;
                 tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
-                const int m0 = (tm * CG + rank) * GEMM_BM, n0 = tn * TILE_N;
-                const int nb = DUAL ? n0 : n0 + rank * C::BN_CTA;   // this CTA's rows of B
+                const int m0 = (tm * 2 + rank) * GEMM_BM, n0 = tn * TILE_N;
+                const int nb = DUAL ? n0 : n0 + rank * (BN / 2);   // this CTA's rows of B
                 for (int kb = 0; kb < p.nk; ++kb) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) {
                         ok = false;
@@ -261,34 +303,28 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                     const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
                     const CUtensorMap* ma = &p.a[second | g];
                     const CUtensorMap* mb = &p.b[second];
-                    uint8_t* sa = smem + s * C::STAGE;
-                    uint8_t* sb = sa + C::A_BYTES;
+                    uint8_t* sa = smem + s * GEMM_STAGE;
+                    uint8_t* sb = sa + GEMM_A_BYTES;
                     auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
-                        if constexpr (CG == 2)
-                            tma_load_2d_pair(dst, map, c0, c1, leader_addr(&full[s]));
-                        else
-                            tma_load_2d(dst, map, c0, c1, &full[s]);
+                        tma_load_2d_pair(dst, map, c0, c1, leader_addr(&full[s]));
                     };
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * GEMM_STAGE);
                     if constexpr (A_MN) {
 #pragma unroll
                         for (int i = 0; i < GEMM_BM / 64; ++i) load(sa + i * BOX_BYTES, ma, m0 + 64 * i, k0);
                     } else {
                         load(sa, ma, k0, m0);
                     }
-                    if constexpr (DUAL && CG == 2) {
+                    if constexpr (DUAL) {
                         load(sb, &p.b[rank], k0, nb);
-                    } else if constexpr (DUAL) {
-                        load(sb, &p.b[0], k0, nb);
-                        load(sb + C::B_BYTES / 2, &p.b[1], k0, nb);
                     } else if constexpr (B_MN) {
 #pragma unroll
-                        for (int i = 0; i < C::BN_CTA / 64; ++i) load(sb + i * BOX_BYTES, mb, nb + 64 * i, k0);
+                        for (int i = 0; i < BN / 2 / 64; ++i) load(sb + i * BOX_BYTES, mb, nb + 64 * i, k0);
                     } else {
                         load(sb, mb, k0, nb);
                     }
                     ++done;
-                    if (++s == C::STAGES) {
+                    if (++s == GEMM_STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -297,11 +333,11 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
             // let the loads in flight land before the shared memory goes away (with a pair, the even CTA's barriers
             // count both CTAs' loads, and neither leaves before both are here)
             if (!ok && rank == 0) {
-                const int n = done < C::STAGES ? done : C::STAGES;
+                const int n = done < GEMM_STAGES ? done : GEMM_STAGES;
                 const uint64_t until = globaltimer_ns() + 2000000000ull;
                 for (int i = 1; i <= n; ++i) {
                     const int j = done - i;
-                    mbar_wait_until(&full[j % C::STAGES], (j / C::STAGES) & 1u, until);
+                    mbar_wait_until(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1u, until);
                 }
             }
         }
@@ -313,8 +349,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
             for (int t = first; ok && t < n_tiles; t += step, ++it) {
                 const int buf = it & 1;
                 const uint32_t drained = ((it >> 1) & 1) ^ 1u;
-                if (!(CG == 2 ? mbar_wait_cluster(&acc_empty[buf], drained, p.err)
-                              : mbar_wait(&acc_empty[buf], drained, p.err))) {
+                if (!mbar_wait_cluster(&acc_empty[buf], drained, p.err)) {
                     ok = false;
                     break;
                 }
@@ -325,22 +360,22 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * C::STAGE));
-                    const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * C::STAGE + C::A_BYTES));
+                    const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
+                    const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
 #pragma unroll
                     for (int k = 0; k < GEMM_BK / 16; ++k)
-                        tc_mma<CG>(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
+                        tc_mma<2>(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
                                kb > 0 || k > 0);
-                    tc_commit<CG>(&empty[s]);
-                    if (++s == C::STAGES) {
+                    tc_commit<2>(&empty[s]);
+                    if (++s == GEMM_STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (ok) tc_commit<CG>(&acc_full[buf]);
+                if (ok) tc_commit<2>(&acc_full[buf]);
             }
             if (!ok) {   // the products in flight end before TMEM is freed
-                tc_commit<CG>(&drain);
+                tc_commit<2>(&drain);
                 mbar_wait_until(&drain, 0, globaltimer_ns() + 2000000000ull);
             }
         }
@@ -355,10 +390,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
         constexpr int HALF = TILE_N / 2;
         const int q = warp & 3, ew = warp - 2, half = ew >> 2;
         const bool f32 = p.out_dt == 2;
-        const int box = epi_box_cols(EPI, BN, f32);
+        const int box = epi_box_cols(EPI, f32);
         const int row_bytes = (f32 || box == 64) ? 128 : 64;
         const uint32_t box_bytes = 32u * row_bytes;
-        uint8_t* buf = smem + C::STAGES * C::STAGE + ew * EPI_BUF;
+        uint8_t* buf = smem + GEMM_STAGES * GEMM_STAGE + ew * EPI_BUF;
         uint8_t* buf2 = buf + EPI_BUF / 2;   // EPI_GATED_BWD: the second output
         uint32_t aux_ph = 0;
         int it = 0;
@@ -368,7 +403,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
             const int g = t / per_group, r = t - g * per_group;
             int tm, tn;
             tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
-            const int row0 = (tm * CG + rank) * GEMM_BM + 32 * q, n0 = tn * TILE_N + half * HALF;
+            const int row0 = (tm * 2 + rank) * GEMM_BM + 32 * q, n0 = tn * TILE_N + half * HALF;
             const int row = row0 + lane;
             const bool live = row < p.M;
             const int64_t row64 = row;
@@ -404,12 +439,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                 if (c + 32 >= HALF) {   // the accumulators have been read
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2)
-                            mbar_arrive_cluster(leader_addr(&acc_empty[ab]));
-                        else
-                            mbar_arrive(&acc_empty[ab]);
-                    }
+                    if (lane == 0) mbar_arrive_cluster(leader_addr(&acc_empty[ab]));
                 }
                 float x[32];
                 if (p.aux && some) {
@@ -425,40 +455,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                     }
                 }
                 if (some) {
-                    if constexpr (!DUAL) {
-                        if (p.bias) {
-                            float b[32];
-                            row_load32(p.bias, col, p.bias_dt, n, b);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += b[i];
-                        }
-                    }
-                    with_act(p.act, [&](auto tag) {
-                        constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if constexpr (EPI == EPI_LINEAR) {
-                                v[i] = act_value<ACT>(v[i]);
-                            } else if constexpr (EPI == EPI_GATED) {
-                                v[i] = act_value<ACT>(v[i]) * u[i];
-                            } else {
-                                float f, df;
-                                act_both<ACT>(v[i], f, df);
-                                if constexpr (EPI == EPI_LINEAR_BWD) {
-                                    v[i] = live && i < n ? x[i] * df : 0.0f;
-                                } else {
-                                    v[i] = x[i] * u[i] * df;
-                                    u[i] = x[i] * f;
-                                }
-                            }
-                        }
-                    });
-                    if constexpr (EPI == EPI_LINEAR) {
-                        if (p.aux) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += x[i];
-                        }
-                    }
+                    piece_math<EPI>(p, col, n, live, x, v, u);
                     if (p.staged) {
                         put32(p.out_dt, v, [&](int i) { return at(buf, c, i); });
                         if constexpr (EPI == EPI_GATED_BWD) put32(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
@@ -468,10 +465,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
                             row_store32(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
                     }
                     if constexpr (EPI == EPI_LINEAR_BWD) {
-                        if (p.colsum) {
-                            const float sum = column_sum32(v, lane);
-                            if (lane < n) p.colsum[static_cast<int64_t>(row0 / 32) * p.N + col + lane] = sum;
-                        }
+                        if (p.colsum) piece_colsum(p, row0, col, n, lane, v);
                     }
                 }
                 if (p.staged && ((c + 32) & (box - 1)) == 0) {
@@ -493,12 +487,187 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(GEMM_THREADS, 1) ge
     }
     __syncwarp();
     tc_fence_before();
-    if constexpr (CG == 2)
-        cluster_sync();
-    else
-        __syncthreads();
+    cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc<CG>(tmem, C::TMEM_COLS);
+    if (warp == 1) tmem_dealloc<2>(tmem, 2 * BN);
+}
+
+// ---------------------------------------------------------------- split kernel
+// Products whose 128 x 128 tiles do not fill the GPU: a cluster of S CTAs
+// computes one tile, each a part of the contraction, and the parts meet in
+// shared memory: every CTA writes its accumulators there (FP32), and each
+// piece of 32 rows x 32 columns is summed in rank order by one warp of the
+// cluster, which runs the epilogue on it.  Nothing passes through HBM and one
+// launch does it.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank)
+{
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __grid_constant__ GemmParams p)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+    constexpr int BN = 128, TILE_N = DUAL ? BN / 2 : BN;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[GEMM_STAGES], empty[GEMM_STAGES], acc_full;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.split, rank = blockIdx.x % S;   // (the cluster's ranks are consecutive blocks)
+    const int t = blockIdx.x / S;
+    const int per_group = p.tiles_m * p.tiles_n;
+    const int g = t / per_group, r = t - g * per_group;
+    int tm, tn;
+    tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = tm * GEMM_BM, n0 = tn * TILE_N;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.nk) * rank / S);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.nk) * (rank + 1) / S);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < GEMM_STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&acc_full, 1);
+        failed = 0;
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == 1) tmem_alloc<1>(&tmem_slot, BN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int done = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++done) {
+                const int s = done % GEMM_STAGES;
+                if (done >= GEMM_STAGES && !mbar_wait(&empty[s], (done / GEMM_STAGES - 1) & 1, p.err)) {
+                    ok = false;
+                    break;
+                }
+                const int second = kb >= p.nk0;
+                const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
+                const CUtensorMap* ma = &p.a[second | g];
+                const CUtensorMap* mb = &p.b[second];
+                uint8_t* sa = smem + s * GEMM_STAGE;
+                uint8_t* sb = sa + GEMM_A_BYTES;
+                mbar_arrive_expect_tx(&full[s], GEMM_STAGE);
+                if constexpr (A_MN) {
+                    tma_load_2d(sa, ma, m0, k0, &full[s]);
+                    tma_load_2d(sa + BOX_BYTES, ma, m0 + 64, k0, &full[s]);
+                } else {
+                    tma_load_2d(sa, ma, k0, m0, &full[s]);
+                }
+                if constexpr (DUAL) {
+                    tma_load_2d(sb, &p.b[0], k0, n0, &full[s]);
+                    tma_load_2d(sb + GEMM_A_BYTES / 2, &p.b[1], k0, n0, &full[s]);
+                } else if constexpr (B_MN) {
+                    tma_load_2d(sb, mb, n0, k0, &full[s]);
+                    tma_load_2d(sb + BOX_BYTES, mb, n0 + 64, k0, &full[s]);
+                } else {
+                    tma_load_2d(sb, mb, k0, n0, &full[s]);
+                }
+            }
+            if (!ok) {   // let the loads in flight land before the shared memory goes away
+                failed = 1;
+                const uint64_t until = globaltimer_ns() + 2000000000ull;
+                for (int j = done > GEMM_STAGES ? done - GEMM_STAGES : 0; j < done; ++j)
+                    mbar_wait_until(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1, until);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int i = 0; i < kb1 - kb0; ++i) {
+                const int s = i % GEMM_STAGES;
+                if (!mbar_wait(&full[s], (i / GEMM_STAGES) & 1, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
+                const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
+#pragma unroll
+                for (int k = 0; k < GEMM_BK / 16; ++k)
+                    tc_mma<1>(tmem, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc, i > 0 || k > 0);
+                tc_commit<1>(&empty[s]);
+            }
+            tc_commit<1>(&acc_full);
+            if (!ok) {   // the products in flight end before TMEM is freed
+                failed = 1;
+                mbar_wait_until(&acc_full, 0, globaltimer_ns() + 2000000000ull);
+            }
+        }
+    }
+    __syncwarp();
+    // accumulators to shared memory, [column][row], over the operand ring (every product has read it by now)
+    float* acc_s = reinterpret_cast<float*>(smem);
+    if (warp >= 2) {
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        if (!mbar_wait(&acc_full, 0, p.err)) failed = 1;
+        tc_fence_after();
+        __syncwarp();
+        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+            float v[32];
+            tmem_ld32(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc_s[(c + i) * GEMM_BM + 32 * q + lane] = v[i];
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && !failed) {
+        constexpr int PIECES = 4 * (TILE_N / 32);
+        for (int u0 = rank + S * (warp - 2); u0 < PIECES; u0 += S * GEMM_EPI_WARPS) {
+            const int q = u0 & 3, c = (u0 >> 2) * 32;
+            const int col = n0 + c, row0 = m0 + 32 * q, row = row0 + lane, n = p.N - col;
+            if (n <= 0 || row0 >= p.M) continue;
+            const bool live = row < p.M;
+            const int64_t row64 = row;
+            float x[32], v[32], u[DUAL ? 32 : 1];
+            if (p.aux && live) row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
+            const uint32_t at = smem_u32(acc_s + c * GEMM_BM + 32 * q + lane);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = ld_cluster(at + i * GEMM_BM * 4, 0);
+            for (int k = 1; k < S; ++k)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += ld_cluster(at + i * GEMM_BM * 4, k);
+            if constexpr (DUAL) {
+                const uint32_t up = at + TILE_N * GEMM_BM * 4;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = ld_cluster(up + i * GEMM_BM * 4, 0);
+                for (int k = 1; k < S; ++k)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] += ld_cluster(up + i * GEMM_BM * 4, k);
+            }
+            piece_math<EPI>(p, col, n, live, x, v, u);
+            if (live) {
+                row_store32(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
+                if constexpr (EPI == EPI_GATED_BWD) row_store32(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
+            }
+            if constexpr (EPI == EPI_LINEAR_BWD) {
+                if (p.colsum) piece_colsum(p, row0, col, n, lane, v);
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // the others have read this CTA's accumulators
+    if (warp == 1) tmem_dealloc<1>(tmem, BN);
 }
 
 }  // namespace qta

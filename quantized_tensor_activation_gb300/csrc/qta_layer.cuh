@@ -22,12 +22,12 @@ cudaError_t launch_col_finish(const float* part, int64_t stride, int parts, int6
 enum GemmForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 
 // Tile of a product: output rows and columns, rows of the TMA box of a
-// contraction-contiguous B, CTAs that share it, columns of its accumulator.
+// contraction-contiguous B, CTAs that split its contraction (0: a pair's tile).
 struct GemmTile {
-    int rows, cols, b_box, cg, bn;
+    int rows, cols, b_box, split;
 };
-GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int groups, int sms);
-cudaError_t launch_gemm(int form, int epi, const GemmTile& t, const GemmParams& p, int sms, cudaStream_t stream);
+GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms);
+cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
 
 // Products of up to SKINNY_ROWS tokens (qta_skinny.cu).
 constexpr int64_t SKINNY_ROWS = 16;

@@ -180,7 +180,10 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
     int sms = 0;
     if (query_device(&sms, &p.err) != cudaSuccess) return QTA_ERR_CUDA;
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const GemmTile t = gemm_tile(form, epi, M, N, groups, sms);
+    p.nk0 = p.nk = static_cast<int>(ceil_div(K, GEMM_BK));
+    if (a1 && groups == 1 && !dual) p.nk *= 2;
+    const GemmTile t = gemm_tile(form, epi, M, N, p.nk, groups, sms);
+    p.split = t.split;
     const int a_rows = form == FORM_TN ? 64 : GEMM_BM;
     const int b_rows = form == FORM_NT ? t.b_box : 64;
     if (!map_mat(&p.a[0], *a0, a_rows) || !map_mat(&p.b[0], *b0, b_rows)) return QTA_ERR_CUDA;
@@ -188,8 +191,6 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
     if (b1 && !map_mat(&p.b[1], *b1, b_rows)) return QTA_ERR_CUDA;
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
-    p.nk0 = p.nk = static_cast<int>(ceil_div(K, GEMM_BK));
-    if (a1 && groups == 1 && !dual) p.nk *= 2;
     p.tiles_m = static_cast<int>(ceil_div(M, t.rows));
     p.tiles_n = static_cast<int>(ceil_div(N, t.cols));
     p.groups = groups;
@@ -205,15 +206,15 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
         p.ld_aux = o.aux->ld;
         p.aux_dt = p.out_dt;
     }
-    p.staged = tma_ok(*o.out0) && (!o.out1 || tma_ok(*o.out1)) && (!o.aux || tma_ok(*o.aux));
+    p.staged = !t.split && tma_ok(*o.out0) && (!o.out1 || tma_ok(*o.out1)) && (!o.aux || tma_ok(*o.aux));
     if (p.staged) {
-        const int box = epi_box_cols(epi, t.bn, p.out_dt == QTA_FP32);
+        const int box = epi_box_cols(epi, p.out_dt == QTA_FP32);
         if (!map_epi(&p.out_map[0], *o.out0, box) || (o.out1 && !map_epi(&p.out_map[1], *o.out1, box)) ||
             (o.aux && !map_epi(&p.aux_map, *o.aux, box)))
             return QTA_ERR_CUDA;
     }
     p.idesc = idesc_f16(0, 0, dt == QTA_BF16, false, false);   // the launcher adds the tile
-    return cuda_status(launch_gemm(form, epi, t, p, sms, s));
+    return cuda_status(launch_gemm(form, epi, p, sms, s));
 }
 
 // The same for few rows.
