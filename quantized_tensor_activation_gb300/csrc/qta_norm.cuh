@@ -20,6 +20,7 @@ struct NormParams {
     float eps;
     int dt, w_dt, rms;
     int shift;              // elements from a 16-byte boundary to row 0
+    int w_smem;             // gamma and beta are kept in shared memory
     int aligned, w_vec;     // rows are whole aligned vectors; gamma and beta are 16-byte aligned
 };
 
@@ -38,7 +39,7 @@ struct NormBwdParams {
     int64_t ld_dy, ld_s, ld_ds, ld_dx;
     int parts;
     int dt, w_dt, rms;
-    int shift, aligned, w_vec;   // as above
+    int shift, aligned, w_vec, w_smem;   // as above
 };
 
 }  // namespace qta

@@ -5,12 +5,12 @@ namespace qta {
 
 cudaError_t launch_norm_rows_fp16(const NormParams& p, const RowPlan& q, int sms, cudaStream_t stream)
 {
-    return pick_row_kernel<1>(p, q, RunFwd{p, q, sms, stream});
+    return pick_row_kernel<1>(p.aligned, p.residual, p.cols, q, RunFwd{p, q, sms, stream});
 }
 
 cudaError_t launch_norm_bwd_rows_fp16(const NormBwdParams& p, const RowPlan& q, cudaStream_t stream)
 {
-    return pick_row_kernel<1>(p, q, RunBwd{p, q, stream});
+    return pick_row_kernel<1>(p.aligned, p.dsum, p.cols, q, RunBwd{p, q, stream});
 }
 
 }  // namespace qta

@@ -1,16 +1,23 @@
-// qta_norm_rows.cuh -- norm kernels that hold a row in registers.
+// qta_norm_rows.cuh -- norm kernels that read each byte once.
 //
-// Forward and backward read each byte once: a thread keeps VPT 16-byte
-// vectors of its row, the statistics come from registers (the variance about
-// the mean, in a second pass over registers), and the next row's vectors are
-// on their way meanwhile.  What bounds them is HBM.
+// T threads (whole warps) work on a row, VPT 16-byte vectors each; a CTA works
+// on G rows at a time.  The rows to come wait in shared memory: every thread
+// copies its own vectors of the next STAGES - 1 rows there asynchronously and
+// reads them back itself, so this ring needs no barrier and no registers.
+// What bounds the kernels is HBM, closely followed by instruction issue (a
+// first form with scalar arithmetic and a test per vector took 1056
+// instructions for four vectors of a row and reached 4.3 TB/s): arithmetic is
+// on pairs of FP32 values, gamma and beta are widened once into shared memory,
+// each thread's own columns, and the loops have no tests but for vectors that
+// cross a row's end.
 //
 // Rows may start anywhere: where every matrix of a call has its rows at the
 // same distance from a 16-byte boundary (one base alignment, row distances
 // equal modulo a vector), vector v of a row holds the columns
 // v * VEC - shift ... with shift that row's distance, so that all vectors but
-// the first and last are aligned, whole ones.  AL: shift is 0 and cols whole
-// vectors.
+// the first and last are aligned, whole ones.  A thread's rows all have one
+// shift: the grid steps over rows in multiples of a vector's elements, or
+// every row has the same.  FULL: shift is 0 and every thread's vectors are whole.
 #pragma once
 
 #include "qta_layer.cuh"
@@ -21,222 +28,133 @@ template <int DT>
 struct Vec {
     static constexpr int N = DT == 2 ? 4 : 8;
     static constexpr int ES = DT == 2 ? 4 : 2;
+    static constexpr int P = N / 2;   // pairs
 
-    static __device__ __forceinline__ void unpack(const uint4 w, float (&f)[N])
+    static __device__ __forceinline__ void unpack(const uint4 w, u64 (&f)[P])
+    {
+        if constexpr (DT == 2) {
+            f[0] = pk2(__uint_as_float(w.x), __uint_as_float(w.y));
+            f[1] = pk2(__uint_as_float(w.z), __uint_as_float(w.w));
+        } else {
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = DT == 0 ? bf16x2_to_pair(ws[j]) : f16x2_to_pair(ws[j]);
+        }
+    }
+
+    static __device__ __forceinline__ uint4 pack(const u64 (&f)[P])
+    {
+        if constexpr (DT == 2) {
+            const float2 a = up2(f[0]), b = up2(f[1]);
+            return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+        } else if constexpr (DT == 0) {
+            return make_uint4(pair_to_bf16x2(f[0]), pair_to_bf16x2(f[1]), pair_to_bf16x2(f[2]), pair_to_bf16x2(f[3]));
+        } else {
+            return make_uint4(pair_to_f16x2(f[0]), pair_to_f16x2(f[1]), pair_to_f16x2(f[2]), pair_to_f16x2(f[3]));
+        }
+    }
+
+    // The vector of columns c0 ... of a row that crosses one of its ends,
+    // zeros outside [0, cols).
+    static __device__ __forceinline__ uint4 load_part(const uint8_t* row, int c0, int cols)
+    {
+        uint32_t ws[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (c0 + k >= 0 && c0 + k < cols) {
+                if constexpr (DT == 2)
+                    ws[k] = reinterpret_cast<const uint32_t*>(row)[c0 + k];
+                else
+                    ws[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[c0 + k]) << (16 * (k & 1));
+            }
+        return make_uint4(ws[0], ws[1], ws[2], ws[3]);
+    }
+
+    static __device__ __forceinline__ void store_part(uint8_t* row, int c0, int cols, const uint4 w)
     {
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == 2) {
-                f[j] = __uint_as_float(ws[j]);
-            } else {
-                const float2 t = unpack2(ws[j], DT);
-                f[2 * j] = t.x;
-                f[2 * j + 1] = t.y;
+        for (int k = 0; k < N; ++k)
+            if (c0 + k >= 0 && c0 + k < cols) {
+                if constexpr (DT == 2)
+                    reinterpret_cast<uint32_t*>(row)[c0 + k] = ws[k];
+                else
+                    reinterpret_cast<uint16_t*>(row)[c0 + k] = static_cast<uint16_t>(ws[k / 2] >> (16 * (k & 1)));
             }
-        }
-    }
-
-    static __device__ __forceinline__ uint4 pack(const float (&f)[N])
-    {
-        if constexpr (DT == 2)
-            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                              __float_as_uint(f[3]));
-        else
-            return make_uint4(pack2(f[0], f[1], DT), pack2(f[2], f[3], DT), pack2(f[4], f[5], DT),
-                              pack2(f[6], f[7], DT));
-    }
-
-    // Vector of the columns c0 ... of the row at `row`, zeros outside [0, cols).
-    template <bool AL>
-    static __device__ __forceinline__ uint4 load(const uint8_t* row, int c0, int cols)
-    {
-        if (c0 >= 0 && c0 + N <= cols) return __ldcs(reinterpret_cast<const uint4*>(row + c0 * ES));
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (!AL) {
-            uint32_t* ws = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (c0 + k >= 0 && c0 + k < cols) {
-                    if constexpr (DT == 2)
-                        ws[k] = reinterpret_cast<const uint32_t*>(row)[c0 + k];
-                    else
-                        ws[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[c0 + k])
-                                     << (16 * (k & 1));
-                }
-        }
-        return w;
-    }
-
-    template <bool AL>
-    static __device__ __forceinline__ void store(uint8_t* row, int c0, int cols, const float (&f)[N])
-    {
-        const uint4 w = pack(f);
-        if (c0 >= 0 && c0 + N <= cols) {
-            *reinterpret_cast<uint4*>(row + c0 * ES) = w;
-        } else if constexpr (!AL) {
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (c0 + k >= 0 && c0 + k < cols) {
-                    if constexpr (DT == 2)
-                        reinterpret_cast<uint32_t*>(row)[c0 + k] = ws[k];
-                    else
-                        reinterpret_cast<uint16_t*>(row)[c0 + k] = static_cast<uint16_t>(ws[k / 2] >> (16 * (k & 1)));
-                }
-        }
     }
 
     // gamma or beta of the columns c0 ..., zeros outside.  `vec`: 16-byte aligned.
-    template <bool AL>
-    static __device__ __forceinline__ void weights(const void* w, int w_dt, bool vec, int c0, int cols, float (&f)[N])
+    template <bool FULL>
+    static __device__ __forceinline__ void weights(const void* w, int w_dt, bool vec, int c0, int cols, u64 (&f)[P])
     {
-        if (AL && vec) {
-            if (c0 < cols) {
-                if (w_dt == DT) {
-                    unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + c0 * ES)), f);
-                } else {   // fp32 weights of a 16-bit activation
-                    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c0);
-#pragma unroll
-                    for (int j = 0; j < N / 4; ++j) {
-                        const float4 t = __ldg(q + j);
-                        f[4 * j] = t.x;
-                        f[4 * j + 1] = t.y;
-                        f[4 * j + 2] = t.z;
-                        f[4 * j + 3] = t.w;
-                    }
-                }
-                return;
-            }
-#pragma unroll
-            for (int k = 0; k < N; ++k) f[k] = 0.0f;
+        if (FULL && vec && w_dt == DT) {
+            unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + c0 * ES)), f);
             return;
         }
 #pragma unroll
-        for (int k = 0; k < N; ++k) f[k] = c0 + k >= 0 && c0 + k < cols ? load_elem(w, c0 + k, w_dt) : 0.0f;
+        for (int j = 0; j < P; ++j) {
+            float v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = c0 + 2 * j + k;
+                v[k] = c >= 0 && c < cols ? load_elem(w, c, w_dt) : 0.0f;
+            }
+            f[j] = pk2(v[0], v[1]);
+        }
+    }
+
+    // The same into N / 4 pieces `pitch` apart in shared memory, and back.
+    static __device__ __forceinline__ void widen(float4* dst, int pitch, const u64 (&f)[P])
+    {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const float2 a = up2(f[2 * j]), b = up2(f[2 * j + 1]);
+            dst[j * pitch] = make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
+
+    static __device__ __forceinline__ void widened(const float4* src, int pitch, u64 (&f)[P])
+    {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const float4 t = src[j * pitch];
+            f[2 * j] = pk2(t.x, t.y);
+            f[2 * j + 1] = pk2(t.z, t.w);
+        }
     }
 };
 
-// A CTA works on G rows at a time, T threads (whole warps) on each.
-constexpr int FWD_MAX_THREADS = 512;
-constexpr int BWD_MAX_THREADS = 640;   // 96 registers: two rows of 5120 16-bit channels at a time
-constexpr int MAX_GROUPS = 16;
-
-// Sums of two values over the T threads of a row's group.  `buf` alternates
-// from call to call, so that one barrier suffices.
-__device__ __forceinline__ void row_sums(float& a, float& b, int T, int group, float2 (*scratch)[BWD_MAX_THREADS / 32],
-                                         int& buf)
+__device__ __forceinline__ float sum2(u64 v)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (T == 32) return;
-    if ((threadIdx.x & 31) == 0) scratch[buf][threadIdx.x >> 5] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
-    const int n = T >> 5, w0 = group * n;
-    a = b = 0.0f;
-    for (int w = 0; w < n; ++w) {
-        const float2 t = scratch[buf][w0 + w];
-        a += t.x;
-        b += t.y;
-    }
-    buf ^= 1;
+    const float2 f = up2(v);
+    return f.x + f.y;
 }
 
-template <int DT, int VPT, bool AL>
-__global__ void __launch_bounds__(FWD_MAX_THREADS, VPT == 2 ? 2 : 1) norm_fwd_kernel(const NormParams p, const int T)
+__device__ __forceinline__ float warp_sum(float v)
 {
-    using V = Vec<DT>;
-    constexpr int N = V::N;
-    __shared__ float2 scratch[2][BWD_MAX_THREADS / 32];
-    int buf = 0;
-    const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T;
-    const int64_t first = blockIdx.x * int64_t(G) + group, step = gridDim.x * int64_t(G);
-    const int cols = static_cast<int>(p.cols);
-    const uint8_t* x = static_cast<const uint8_t*>(p.x);
-    const uint8_t* res = static_cast<const uint8_t*>(p.residual);
-    const float inv = 1.0f / static_cast<float>(cols);
-    pdl_wait();
-    pdl_trigger();
-
-    uint4 nx[VPT], nr[VPT];
-    auto shift_of = [&](int64_t r) { return AL ? 0 : static_cast<int>((p.shift + r * p.ld_x) & (N - 1)); };
-    auto fetch = [&](int64_t r) {
-        const int sh = shift_of(r);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c0 = (tid + i * T) * N - sh;
-            nx[i] = V::template load<AL>(x + r * p.ld_x * V::ES, c0, cols);
-            if (res) nr[i] = V::template load<AL>(res + r * p.ld_r * V::ES, c0, cols);
-        }
-    };
-    if (first < p.rows) fetch(first);
-    for (int64_t r = first; r < p.rows; r += step) {
-        const int sh = shift_of(r);
-        float s[VPT][N];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            V::unpack(nx[i], s[i]);
-            if (res) {
-                float t[N];
-                V::unpack(nr[i], t);
-#pragma unroll
-                for (int k = 0; k < N; ++k) s[i][k] += t[k];
-            }
-        }
-        if (r + step < p.rows) fetch(r + step);
-        float mean = 0.0f, dummy = 0.0f;
-        if (!p.rms) {
-            float a = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int k = 0; k < N; ++k) a += s[i][k];
-            row_sums(a, dummy, T, group, scratch, buf);
-            mean = a * inv;
-        }
-        float q = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c0 = (tid + i * T) * N - sh;
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float d = s[i][k] - mean;
-                if (AL ? c0 < cols : (c0 + k >= 0 && c0 + k < cols)) q = fmaf(d, d, q);
-            }
-        }
-        row_sums(q, dummy, T, group, scratch, buf);
-        const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c0 = (tid + i * T) * N - sh;
-            if (c0 >= cols) continue;
-            float g[N], o[N];
-            if (p.sum) V::template store<AL>(static_cast<uint8_t*>(p.sum) + r * p.ld_s * V::ES, c0, cols, s[i]);
-            V::template weights<AL>(p.gamma, p.w_dt, p.w_vec, c0, cols, g);
-#pragma unroll
-            for (int k = 0; k < N; ++k) o[k] = (s[i][k] - mean) * rstd * g[k];
-            if (p.beta) {
-                V::template weights<AL>(p.beta, p.w_dt, p.w_vec, c0, cols, g);
-#pragma unroll
-                for (int k = 0; k < N; ++k) o[k] += g[k];
-            }
-            V::template store<AL>(static_cast<uint8_t*>(p.y) + r * p.ld_y * V::ES, c0, cols, o);
-        }
-        if (tid == 0) {
-            if (p.mean) p.mean[r] = mean;
-            if (p.rstd) p.rstd[r] = rstd;
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// One 16-byte piece into shared memory; the calling thread alone reads it,
-// after cp_wait.
-__device__ __forceinline__ void cp_async16(uint4* dst, const void* src)
+// One 16-byte piece into shared memory where `on` (the calling thread alone
+// reads it, after cp_wait), and one out: predicated, so that a row's accesses
+// are issued without a branch between.
+__device__ __forceinline__ void cp_async16(uint4* dst, const void* src, bool on)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(on ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void st16(void* dst, const uint4 w, bool on)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q st.global.v4.u32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(dst),
+        "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w), "r"(on ? 1u : 0u)
+        : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -244,116 +162,400 @@ __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void group_sync(int group, int T)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
+}
 
-// Backward: dx of each row, and the CTA's share of dgamma and dbeta kept in
-// registers over its rows (a CTA's rows have one shift: the grid is a
-// multiple of a vector's elements, or every row has the same), then written
-// as row blockIdx.x of the partial sums.
-//
-// Registers hold those sums (VPT vectors of two), so the rows in flight wait
-// in shared memory instead: every thread copies its own vectors of the next
-// BWD_STAGES - 1 rows there asynchronously and reads them back itself, without
-// a barrier.
+constexpr int FWD_MAX_THREADS = 512;
+template <bool RES>
+constexpr int FWD_STAGES = RES ? 2 : 4;
+constexpr int BWD_MAX_THREADS = 640;   // 96 registers: two rows of 5120 16-bit channels at a time
 template <int VPT>
 constexpr int BWD_STAGES = VPT == 2 ? 3 : 2;
+constexpr int MAX_GROUPS = 16;
+constexpr int ROW_SMEM = 226 * 1024;   // dynamic shared memory of a CTA (227 KB less the static part)
 
-template <int DT, int VPT, bool AL>
-__global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const NormBwdParams p, const int T)
+// This thread's vectors: the columns they start at, and which are whole or
+// touch the row at all (bit i: vector i).
+template <int DT, int VPT, bool FULL>
+struct Span {
+    int c0;   // of vector 0; vector i: T * N further each
+    uint32_t whole, any;
+    __device__ __forceinline__ Span(int tid, int T, int shift, int cols)
+    {
+        constexpr int N = Vec<DT>::N;
+        c0 = tid * N - shift;
+        whole = any = (1u << VPT) - 1;
+        if (!FULL) {
+            whole = any = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = c0 + i * T * N;
+                whole |= static_cast<uint32_t>(c >= 0 && c + N <= cols) << i;
+                any |= static_cast<uint32_t>(c < cols) << i;
+            }
+        }
+    }
+    __device__ __forceinline__ bool is_whole(int i) const { return FULL || (whole >> i & 1); }
+    __device__ __forceinline__ bool is_any(int i) const { return FULL || (any >> i & 1); }
+    __device__ __forceinline__ bool has_part() const { return !FULL && whole != any; }
+};
+
+// A thread's vectors of a row at `row`, from packed values.
+template <int DT, int VPT, bool FULL>
+__device__ __forceinline__ void store_row(uint8_t* row, int T, int cols, const Span<DT, VPT, FULL>& sp,
+                                          const u64 (&v)[VPT][Vec<DT>::P])
 {
     using V = Vec<DT>;
-    constexpr int N = V::N, S = BWD_STAGES<VPT>;
-    __shared__ float2 scratch[2][BWD_MAX_THREADS / 32];
-    extern __shared__ uint4 stage_s[];   // [S][dy, s, dsum][VPT][threads]; in the end G > 1: [2][cols] sums
-    int buf = 0;
-    const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T;
-    const int64_t first = blockIdx.x + int64_t(gridDim.x) * group, step = gridDim.x * int64_t(G);
-    const int cols = static_cast<int>(p.cols);
-    const uint8_t* mats[3] = {static_cast<const uint8_t*>(p.dy), static_cast<const uint8_t*>(p.s),
-                              static_cast<const uint8_t*>(p.dsum)};
-    const int64_t lds[3] = {p.ld_dy, p.ld_s, p.ld_ds};
-    const int n_mats = p.dsum ? 3 : 2;
-    const float inv = 1.0f / static_cast<float>(cols);
-    pdl_wait();
-    pdl_trigger();
+    uint8_t* at = row + static_cast<int64_t>(sp.c0) * V::ES;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) st16(at + i * T * 16, V::pack(v[i]), sp.is_whole(i));
+    if (sp.has_part()) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (sp.is_any(i) && !sp.is_whole(i)) V::store_part(row, sp.c0 + i * T * V::N, cols, V::pack(v[i]));
+    }
+}
 
-    const int sh = AL ? 0 : static_cast<int>((p.shift + first * p.ld_s) & (N - 1));
-    auto slot = [&](int st, int m, int i) { return stage_s + ((st * n_mats + m) * VPT + i) * blockDim.x + threadIdx.x; };
-    auto fetch = [&](int64_t r, int st) {
-        if (r < p.rows) {
+// The ring of rows: MATS matrices of one shift, this thread's vectors.
+template <int DT, int VPT, bool FULL, int MATS, int STAGES>
+struct Ring {
+    const uint8_t* next[MATS];   // the row to fetch next, at column c0 of vector 0
+    int64_t advance[MATS];       // bytes to this thread's following row
+    uint4* base;
+    int pitch;                   // threads of the CTA
+    int T, cols;
+
+    // Slots of vectors outside the row hold zeros from here on.
+    __device__ __forceinline__ void clear(const Span<DT, VPT, FULL>& sp)
+    {
 #pragma unroll
-            for (int m = 0; m < 3; ++m) {
-                if (m == n_mats) break;
-                const uint8_t* row = mats[m] + r * lds[m] * V::ES;
+        for (int st = 0; st < STAGES; ++st)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int c0 = (tid + i * T) * N - sh;
-                    if (c0 >= 0 && c0 + N <= cols)
-                        cp_async16(slot(st, m, i), row + c0 * V::ES);
-                    else
-                        *slot(st, m, i) = V::template load<AL>(row, c0, cols);
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (!sp.is_any(i)) *slot(st, m, i) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ uint4* slot(int st, int m, int i) const
+    {
+        return base + ((st * MATS + m) * VPT + i) * pitch;
+    }
+    __device__ __forceinline__ void fetch(int st, bool on, const Span<DT, VPT, FULL>& sp)
+    {
+        if (on) {
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) cp_async16(slot(st, m, i), next[m] + i * T * 16, sp.is_whole(i));
+                if (sp.has_part()) {
+                    const uint8_t* row = next[m] - static_cast<int64_t>(sp.c0) * Vec<DT>::ES;
+#pragma unroll
+                    for (int i = 0; i < VPT; ++i)
+                        if (sp.is_any(i) && !sp.is_whole(i))
+                            *slot(st, m, i) = Vec<DT>::load_part(row, sp.c0 + i * T * Vec<DT>::N, cols);
                 }
+                next[m] += advance[m];
             }
         }
         cp_commit();
-    };
-    float dg[VPT][N], db[VPT][N];
+    }
+};
+
+// gamma or beta of this thread's vectors: widened once into shared memory,
+// which the CTA's groups share (their rows have one shift), or, where it has no
+// room, read from global memory each time.
+template <int DT, int VPT, bool FULL>
+struct Weights {
+    const void* w;
+    int w_dt, vec, c0, cols, T;
+    float4* smem;   // NULL: not kept
+    __device__ __forceinline__ void keep(int group)
+    {
+        if (!smem || group) return;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            u64 f[Vec<DT>::P];
+            Vec<DT>::template weights<FULL>(w, w_dt, vec, c0 + i * T * Vec<DT>::N, cols, f);
+            Vec<DT>::widen(smem + i * (Vec<DT>::N / 4) * T, T, f);
+        }
+    }
+    __device__ __forceinline__ void get(int i, u64 (&f)[Vec<DT>::P]) const
+    {
+        if (smem)
+            Vec<DT>::widened(smem + i * (Vec<DT>::N / 4) * T, T, f);
+        else
+            Vec<DT>::template weights<FULL>(w, w_dt, vec, c0 + i * T * Vec<DT>::N, cols, f);
+    }
+};
+
+// Forward.  A warp takes its own mean and sum of squares about it from
+// registers; the row's follow from the warps' (n, mean, M2) exactly:
+// M2 = sum of M2_w + n_w (mean_w - mean)^2, one barrier a row.
+template <int DT, int VPT, bool FULL, bool RES>
+__global__ void __launch_bounds__(FWD_MAX_THREADS, 1) norm_fwd_kernel(const NormParams p, const int T)
+{
+    using V = Vec<DT>;
+    constexpr int N = V::N, P = V::P, S = FWD_STAGES<RES>, MATS = RES ? 2 : 1;
+    __shared__ float4 scratch[2][FWD_MAX_THREADS / 32];
+    extern __shared__ uint4 stage_s[];   // ring [S][MATS][VPT][threads], then gamma, beta [2][VPT * N / 4][T]
+    int buf = 0;
+    const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T, pitch = blockDim.x;
+    const int64_t first = blockIdx.x + int64_t(gridDim.x) * group, step = gridDim.x * int64_t(G);
+    const int cols = static_cast<int>(p.cols), es = V::ES;
+    const float inv = 1.0f / static_cast<float>(cols);
+    const int shift = FULL ? 0 : static_cast<int>((p.shift + first * p.ld_x) & (N - 1));
+    const Span<DT, VPT, FULL> sp(tid, T, shift, cols);
+    Ring<DT, VPT, FULL, MATS, S> ring;
+    ring.base = stage_s + threadIdx.x;
+    ring.pitch = pitch;
+    ring.T = T;
+    ring.cols = cols;
+    ring.next[0] = static_cast<const uint8_t*>(p.x) + (first * p.ld_x + sp.c0) * es;
+    ring.advance[0] = step * p.ld_x * es;
+    if constexpr (RES) {
+        ring.next[1] = static_cast<const uint8_t*>(p.residual) + (first * p.ld_r + sp.c0) * es;
+        ring.advance[1] = step * p.ld_r * es;
+    }
+    uint8_t* y = static_cast<uint8_t*>(p.y) + first * p.ld_y * es;
+    uint8_t* sum = static_cast<uint8_t*>(p.sum) + first * p.ld_s * es;
+    float4* ws = p.w_smem ? reinterpret_cast<float4*>(stage_s + S * MATS * VPT * pitch) + tid : nullptr;
+    Weights<DT, VPT, FULL> ga{p.gamma, p.w_dt, p.w_vec, sp.c0, cols, T, ws};
+    Weights<DT, VPT, FULL> be{p.beta, p.w_dt, p.w_vec, sp.c0, cols, T, ws ? ws + VPT * (N / 4) * T : nullptr};
+    pdl_wait();
+    pdl_trigger();
+
+    ring.clear(sp);
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) ring.fetch(j, first + j * step < p.rows, sp);
+    ga.keep(group);
+    if (p.beta) be.keep(group);
+    __syncthreads();
+    int count = FULL ? VPT * N : 0;
+    if (!FULL) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = sp.c0 + i * T * N;
+            if (sp.is_any(i)) count += min(c + N, cols) - max(c, 0);
+        }
+    }
+    const float n = static_cast<float>(__reduce_add_sync(0xffffffffu, count));   // columns of this warp
+    const float inv_n = n > 0.0f ? 1.0f / n : 0.0f;
+    int st = 0;
+    for (int64_t r = first; r < p.rows; r += step) {
+        ring.fetch(st == 0 ? S - 1 : st - 1, r + (S - 1) * step < p.rows, sp);
+        cp_wait<S - 1>();
+        u64 s[VPT][P];
+        u64 a2 = pk2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            V::unpack(*ring.slot(st, 0, i), s[i]);
+            if constexpr (RES) {
+                u64 t[P];
+                V::unpack(*ring.slot(st, 1, i), t);
+#pragma unroll
+                for (int j = 0; j < P; ++j) s[i][j] = add2(s[i][j], t[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) a2 = add2(a2, s[i][j]);
+        }
+        float mean = p.rms ? 0.0f : warp_sum(sum2(a2)) * inv_n;
+        u64 q2 = pk2(0.0f, 0.0f);
+        const u64 m2 = pk2(mean, mean);
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            // vectors that are not whole: 0 here, their columns are added below
+            const float on = sp.is_whole(i) ? 1.0f : 0.0f;
+            const u64 on2 = pk2(on, on), off2 = pk2(-mean * on, -mean * on);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const u64 d = FULL ? sub2(s[i][j], m2) : fma2(s[i][j], on2, off2);
+                q2 = fma2(d, d, q2);
+            }
+        }
+        if (sp.has_part()) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (sp.is_whole(i) || !sp.is_any(i)) continue;
+                const int c = sp.c0 + i * T * N;
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 d = up2(sub2(s[i][j], m2));
+                    if (c + 2 * j >= 0 && c + 2 * j < cols) q = fmaf(d.x, d.x, q);
+                    if (c + 2 * j + 1 >= 0 && c + 2 * j + 1 < cols) q = fmaf(d.y, d.y, q);
+                }
+            }
+        }
+        q = warp_sum(q + sum2(q2));
+        if (T > 32) {
+            const int W = T >> 5;
+            float4* sc = scratch[buf] + group * W;
+            if ((threadIdx.x & 31) == 0) sc[tid >> 5] = make_float4(mean, q, n, 0.0f);
+            group_sync(group, T);
+            if (!p.rms) {
+                float t = 0.0f;
+                for (int w = 0; w < W; ++w) t = fmaf(sc[w].x, sc[w].z, t);
+                mean = t * inv;
+            }
+            q = 0.0f;
+            for (int w = 0; w < W; ++w) {
+                const float4 e = sc[w];
+                const float d = e.x - mean;
+                q += fmaf(e.z * d, d, e.y);
+            }
+            buf ^= 1;
+        }
+        const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
+        const u64 mm2 = pk2(mean, mean), r2 = pk2(rstd, rstd);
+        if (p.sum) {
+            store_row(sum, T, cols, sp, s);
+            sum += step * p.ld_s * es;
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            u64 g[P];
+            ga.get(i, g);
+#pragma unroll
+            for (int j = 0; j < P; ++j) s[i][j] = mul2(mul2(sub2(s[i][j], mm2), r2), g[j]);
+        }
+        if (p.beta) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                u64 g[P];
+                be.get(i, g);
+#pragma unroll
+                for (int j = 0; j < P; ++j) s[i][j] = add2(s[i][j], g[j]);
+            }
+        }
+        store_row(y, T, cols, sp, s);
+        y += step * p.ld_y * es;
+        if (tid == 0) {
+            if (p.mean) p.mean[r] = mean;
+            if (p.rstd) p.rstd[r] = rstd;
+        }
+        st = st == S - 1 ? 0 : st + 1;
+    }
+    cp_wait<0>();
+}
+
+// Backward: dx of each row, and the CTA's share of dgamma and dbeta kept in
+// registers over its rows, then written as row blockIdx.x of the partial sums.
+template <int DT, int VPT, bool FULL, bool RES>
+__global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const NormBwdParams p, const int T)
+{
+    using V = Vec<DT>;
+    constexpr int N = V::N, P = V::P, S = BWD_STAGES<VPT>, MATS = RES ? 3 : 2;
+    __shared__ float2 scratch[2][BWD_MAX_THREADS / 32];
+    // ring [S][MATS][VPT][threads], then gamma [VPT * N / 4][T]; in the end G > 1: [2][cols] sums
+    extern __shared__ uint4 stage_s[];
+    int buf = 0;
+    const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T, pitch = blockDim.x;
+    const int64_t first = blockIdx.x + int64_t(gridDim.x) * group, step = gridDim.x * int64_t(G);
+    const int cols = static_cast<int>(p.cols), es = V::ES;
+    const float inv = 1.0f / static_cast<float>(cols);
+    const int shift = FULL ? 0 : static_cast<int>((p.shift + first * p.ld_s) & (N - 1));
+    const Span<DT, VPT, FULL> sp(tid, T, shift, cols);
+    Ring<DT, VPT, FULL, MATS, S> ring;
+    ring.base = stage_s + threadIdx.x;
+    ring.pitch = pitch;
+    ring.T = T;
+    ring.cols = cols;
+    ring.next[0] = static_cast<const uint8_t*>(p.dy) + (first * p.ld_dy + sp.c0) * es;
+    ring.advance[0] = step * p.ld_dy * es;
+    ring.next[1] = static_cast<const uint8_t*>(p.s) + (first * p.ld_s + sp.c0) * es;
+    ring.advance[1] = step * p.ld_s * es;
+    if constexpr (RES) {
+        ring.next[2] = static_cast<const uint8_t*>(p.dsum) + (first * p.ld_ds + sp.c0) * es;
+        ring.advance[2] = step * p.ld_ds * es;
+    }
+    uint8_t* dx = static_cast<uint8_t*>(p.dx) + first * p.ld_dx * es;
+    float4* ws = p.w_smem ? reinterpret_cast<float4*>(stage_s + S * MATS * VPT * pitch) + tid : nullptr;
+    Weights<DT, VPT, FULL> ga{p.gamma, p.w_dt, p.w_vec, sp.c0, cols, T, ws};
+    pdl_wait();
+    pdl_trigger();
+
+    ring.clear(sp);
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) ring.fetch(j, first + j * step < p.rows, sp);
+    ga.keep(group);
+    __syncthreads();
+    u64 dg[VPT][P], db[VPT][P];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int k = 0; k < N; ++k) dg[i][k] = db[i][k] = 0.0f;
+        for (int j = 0; j < P; ++j) dg[i][j] = db[i][j] = pk2(0.0f, 0.0f);
     float nmean = 0.0f, nrstd = 0.0f;
     if (first < p.rows) {
         if (!p.rms) nmean = __ldg(p.mean + first);
         nrstd = __ldg(p.rstd + first);
     }
-#pragma unroll
-    for (int j = 0; j < S - 1; ++j) fetch(first + j * step, j);
     int st = 0;
     for (int64_t r = first; r < p.rows; r += step) {
-        const float mean = nmean, rstd = nrstd;
-        fetch(r + (S - 1) * step, st == 0 ? S - 1 : st - 1);
+        const float rstd = nrstd;
+        const u64 mean2 = pk2(nmean, nmean), rstd2 = pk2(rstd, rstd);
+        ring.fetch(st == 0 ? S - 1 : st - 1, r + (S - 1) * step < p.rows, sp);
         if (r + step < p.rows) {
             if (!p.rms) nmean = __ldg(p.mean + r + step);
             nrstd = __ldg(p.rstd + r + step);
         }
         cp_wait<S - 1>();
-        float a = 0.0f, b = 0.0f;
+        u64 a2 = pk2(0.0f, 0.0f), b2 = a2;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c0 = (tid + i * T) * N - sh;
-            float g[N], d[N], xh[N];
-            V::template weights<AL>(p.gamma, p.w_dt, p.w_vec, c0, cols, g);
-            V::unpack(*slot(st, 0, i), d);
-            V::unpack(*slot(st, 1, i), xh);
+            u64 g[P], t[P], xh[P];
+            ga.get(i, g);
+            V::unpack(*ring.slot(st, 0, i), t);
+            V::unpack(*ring.slot(st, 1, i), xh);
 #pragma unroll
-            for (int k = 0; k < N; ++k) {   // (past the row's ends dy and gamma are 0)
-                xh[k] = (xh[k] - mean) * rstd;
-                dg[i][k] = fmaf(d[k], xh[k], dg[i][k]);
-                db[i][k] += d[k];
-                const float t = d[k] * g[k];
-                a += t;
-                b = fmaf(t, xh[k], b);
+            for (int j = 0; j < P; ++j) {   // (past the row's ends dy and gamma are 0)
+                xh[j] = mul2(sub2(xh[j], mean2), rstd2);
+                dg[i][j] = fma2(t[j], xh[j], dg[i][j]);
+                if (!p.rms) db[i][j] = add2(db[i][j], t[j]);
+                t[j] = mul2(t[j], g[j]);
+                a2 = add2(a2, t[j]);
+                b2 = fma2(t[j], xh[j], b2);
             }
         }
-        row_sums(a, b, T, group, scratch, buf);
-        const float mt = p.rms ? 0.0f : a * inv, mtx = b * inv;
+        float b = warp_sum(sum2(b2)), a = p.rms ? 0.0f : warp_sum(sum2(a2));
+        if (T > 32) {
+            const int W = T >> 5;
+            float2* sc = scratch[buf] + group * W;
+            if ((threadIdx.x & 31) == 0) sc[tid >> 5] = make_float2(a, b);
+            group_sync(group, T);
+            a = b = 0.0f;
+            for (int w = 0; w < W; ++w) {
+                const float2 e = sc[w];
+                a += e.x;
+                b += e.y;
+            }
+            buf ^= 1;
+        }
+        const float mt = a * inv, mtx = -(b * inv);
+        const u64 mt2 = pk2(mt, mt), mtx2 = pk2(mtx, mtx);
+        uint8_t* at = dx + static_cast<int64_t>(sp.c0) * es;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c0 = (tid + i * T) * N - sh;
-            if (c0 >= cols) continue;
-            float g[N], d[N], xh[N];
-            V::template weights<AL>(p.gamma, p.w_dt, p.w_vec, c0, cols, g);
-            V::unpack(*slot(st, 0, i), d);
-            V::unpack(*slot(st, 1, i), xh);
+            u64 g[P], t[P], xh[P];   // again from shared memory: the registers hold the columns' sums
+            ga.get(i, g);
+            V::unpack(*ring.slot(st, 0, i), t);
+            V::unpack(*ring.slot(st, 1, i), xh);
 #pragma unroll
-            for (int k = 0; k < N; ++k) d[k] = fmaf(-((xh[k] - mean) * rstd), mtx, d[k] * g[k] - mt) * rstd;
-            if (n_mats == 3) {
-                V::unpack(*slot(st, 2, i), xh);
-#pragma unroll
-                for (int k = 0; k < N; ++k) d[k] += xh[k];
+            for (int j = 0; j < P; ++j) {
+                xh[j] = mul2(sub2(xh[j], mean2), rstd2);
+                t[j] = mul2(fma2(xh[j], mtx2, sub2(mul2(t[j], g[j]), mt2)), rstd2);
             }
-            V::template store<AL>(static_cast<uint8_t*>(p.dx) + r * p.ld_dx * V::ES, c0, cols, d);
+            if constexpr (RES) {
+                V::unpack(*ring.slot(st, 2, i), xh);
+#pragma unroll
+                for (int j = 0; j < P; ++j) t[j] = add2(t[j], xh[j]);
+            }
+            const uint4 w = V::pack(t);
+            st16(at + i * T * 16, w, sp.is_whole(i));
+            if (sp.is_any(i) && !sp.is_whole(i)) V::store_part(dx, sp.c0 + i * T * N, cols, w);
         }
+        dx += step * p.ld_dx * es;
         st = st == S - 1 ? 0 : st + 1;
     }
     cp_wait<0>();
@@ -367,39 +569,43 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
                 for (int i = 0; i < VPT; ++i)
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
-                        const int c = (tid + i * T) * N - sh + k;
+                        const int c = sp.c0 + i * T * N + k;
                         if (c >= 0 && c < cols) {
-                            acc_s[c] = (w ? acc_s[c] : 0.0f) + dg[i][k];
-                            acc_s[cols + c] = (w ? acc_s[cols + c] : 0.0f) + db[i][k];
+                            const float2 vg = up2(dg[i][k / 2]), vb = up2(db[i][k / 2]);
+                            acc_s[c] = (w ? acc_s[c] : 0.0f) + (k & 1 ? vg.y : vg.x);
+                            acc_s[cols + c] = (w ? acc_s[cols + c] : 0.0f) + (k & 1 ? vb.y : vb.x);
                         }
                     }
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) part[c] = acc_s[c];
+        for (int c = threadIdx.x; c < (p.dbeta ? 2 : 1) * cols; c += blockDim.x) part[c] = acc_s[c];
     } else {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const int c = (tid + i * T) * N - sh + k;
+                const int c = sp.c0 + i * T * N + k;
                 if (c >= 0 && c < cols) {
-                    part[c] = dg[i][k];
-                    part[cols + c] = db[i][k];
+                    const float2 vg = up2(dg[i][k / 2]), vb = up2(db[i][k / 2]);
+                    part[c] = k & 1 ? vg.y : vg.x;
+                    if (p.dbeta) part[cols + c] = k & 1 ? vb.y : vb.x;
                 }
             }
     }
 }
 
-// Threads per row, vectors per thread and rows at a time for rows of nv
+// Vectors per thread, threads per row and rows at a time for rows of nv
 // vectors (the first and last of a shifted row included).
 struct RowPlan {
     int vpt, T, G;
 };
 
-inline bool row_plan(int64_t nv, int max_threads, RowPlan* q)
+// Two vectors a thread for the backward's registers (four beyond 1024
+// vectors), four for the forward wherever a row has them.
+inline bool row_plan(int64_t nv, bool bwd, int max_threads, RowPlan* q)
 {
-    q->vpt = nv <= 1024 ? 2 : 4;
+    q->vpt = (bwd ? nv <= 1024 : nv <= 64) ? 2 : 4;
     const int64_t T = ((nv + q->vpt - 1) / q->vpt + 31) / 32 * 32;
     if (T > 512) return false;
     q->T = static_cast<int>(T);
@@ -409,32 +615,55 @@ inline bool row_plan(int64_t nv, int max_threads, RowPlan* q)
     return true;
 }
 
-template <int DT, int VPT, bool AL>
+template <int DT, int VPT, bool FULL, bool RES>
 cudaError_t launch_norm_fwd_1(const NormParams& p, const RowPlan& q, int sms, cudaStream_t stream)
 {
-    const int threads = q.T * q.G;
-    const int64_t units = (p.rows + q.G - 1) / q.G, most = static_cast<int64_t>(sms) * (1024 / threads);
-    return launch_pdl(norm_fwd_kernel<DT, VPT, AL>, dim3(static_cast<unsigned>(units < most ? units : most)),
-                      dim3(threads), 0, stream, p, q.T);
+    NormParams pp = p;
+    int G = q.G;
+    const int weights = VPT * 16 * q.T * (p.beta ? 2 : 1) * (Vec<DT>::N / 4);
+    const auto ring = [&] { return VPT * 16 * q.T * G * FWD_STAGES<RES> * (RES ? 2 : 1); };
+    while (G > 1 && ring() + weights > ROW_SMEM) --G;
+    pp.w_smem = ring() + weights <= ROW_SMEM;
+    const int threads = q.T * G, smem = ring() + (pp.w_smem ? weights : 0);
+    static std::atomic<unsigned> done{0};
+    auto fn = norm_fwd_kernel<DT, VPT, FULL, RES>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem, &done);
+    if (e != cudaSuccess) return e;
+    // one CTA on an SM; steps of whole vectors' elements where rows are shifted
+    const int64_t units = (p.rows + G - 1) / G;
+    int64_t grid = units < sms ? units : sms;
+    if (!FULL) grid = grid > 8 ? grid / 8 * 8 : 8;
+    return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, stream, pp, q.T);
 }
 
-template <int DT, int VPT, bool AL>
+template <int DT, int VPT, bool FULL, bool RES>
 cudaError_t launch_norm_bwd_1(const NormBwdParams& p, const RowPlan& q, cudaStream_t stream)
 {
     // the ring of rows holds the sums of both vectors afterwards: two floats for each element of a row's slots
-    const int smem = BWD_STAGES<VPT> * (p.dsum ? 3 : 2) * VPT * 16 * q.T * q.G;
+    NormBwdParams pp = p;
+    const int ring = VPT * 16 * q.T * q.G * BWD_STAGES<VPT> * (RES ? 3 : 2), weights = VPT * 16 * q.T * (Vec<DT>::N / 4);
+    pp.w_smem = ring + weights <= ROW_SMEM;
+    const int smem = ring + (pp.w_smem ? weights : 0);
     static std::atomic<unsigned> done{0};
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(norm_bwd_kernel<DT, VPT, AL>), smem, &done);
+    auto fn = norm_bwd_kernel<DT, VPT, FULL, RES>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_bwd_kernel<DT, VPT, AL>, dim3(p.parts), dim3(q.T * q.G), smem, stream, p, q.T);
+    return launch_pdl(fn, dim3(p.parts), dim3(q.T * q.G), smem, stream, pp, q.T);
 }
 
-// f.run<DT, VPT, AL>() of the form that the call needs.
-template <int DT, typename P, typename F>
-cudaError_t pick_row_kernel(const P& p, const RowPlan& q, F&& f)
+// f.run<DT, VPT, FULL, RES>() of the form that the call needs.
+template <int DT, int VPT, typename F>
+cudaError_t pick_row_form(bool full, bool res, F&& f)
 {
-    if (q.vpt == 2) return p.aligned ? f.template run<DT, 2, true>() : f.template run<DT, 2, false>();
-    return p.aligned ? f.template run<DT, 4, true>() : f.template run<DT, 4, false>();
+    if (full) return res ? f.template run<DT, VPT, true, true>() : f.template run<DT, VPT, true, false>();
+    return res ? f.template run<DT, VPT, false, true>() : f.template run<DT, VPT, false, false>();
+}
+
+template <int DT, typename F>
+cudaError_t pick_row_kernel(bool aligned, bool res, int64_t cols, const RowPlan& q, F&& f)
+{
+    const bool full = aligned && cols == static_cast<int64_t>(q.T) * q.vpt * Vec<DT>::N;
+    return q.vpt == 2 ? pick_row_form<DT, 2>(full, res, f) : pick_row_form<DT, 4>(full, res, f);
 }
 
 struct RunFwd {
@@ -442,16 +671,16 @@ struct RunFwd {
     const RowPlan& q;
     int sms;
     cudaStream_t s;
-    template <int DT, int VPT, bool AL>
-    cudaError_t run() const { return launch_norm_fwd_1<DT, VPT, AL>(p, q, sms, s); }
+    template <int DT, int VPT, bool FULL, bool RES>
+    cudaError_t run() const { return launch_norm_fwd_1<DT, VPT, FULL, RES>(p, q, sms, s); }
 };
 
 struct RunBwd {
     const NormBwdParams& p;
     const RowPlan& q;
     cudaStream_t s;
-    template <int DT, int VPT, bool AL>
-    cudaError_t run() const { return launch_norm_bwd_1<DT, VPT, AL>(p, q, s); }
+    template <int DT, int VPT, bool FULL, bool RES>
+    cudaError_t run() const { return launch_norm_bwd_1<DT, VPT, FULL, RES>(p, q, s); }
 };
 
 }  // namespace qta
