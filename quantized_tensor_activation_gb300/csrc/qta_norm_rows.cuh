@@ -137,6 +137,22 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// Sum over 16 lanes (each half of the warp its own).
+__device__ __forceinline__ float half_sum(float v)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Two warp sums in the steps of one: the halves of the warp take one value
+// each.  Lanes 0-15 return the sum of a, lanes 16-31 that of b.
+__device__ __forceinline__ float warp_sum_ab(float a, float b, int lane)
+{
+    const bool up = lane & 16;
+    return half_sum((up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16));
+}
+
 // One 16-byte piece into shared memory where `on` (the calling thread alone
 // reads it, after cp_wait), and one out: predicated, so that a row's accesses
 // are issued without a branch between.
@@ -170,7 +186,7 @@ __device__ __forceinline__ void group_sync(int group, int T)
 constexpr int FWD_MAX_THREADS = 512;
 template <bool RES>
 constexpr int FWD_STAGES = RES ? 2 : 4;
-constexpr int BWD_MAX_THREADS = 640;   // 96 registers: two rows of 5120 16-bit channels at a time
+constexpr int BWD_MAX_THREADS = 512;
 template <int VPT>
 constexpr int BWD_STAGES = VPT == 2 ? 3 : 2;
 constexpr int MAX_GROUPS = 16;
@@ -302,6 +318,7 @@ __global__ void __launch_bounds__(FWD_MAX_THREADS, 1) norm_fwd_kernel(const Norm
     extern __shared__ uint4 stage_s[];   // ring [S][MATS][VPT][threads], then gamma, beta [2][VPT * N / 4][T]
     int buf = 0;
     const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T, pitch = blockDim.x;
+    const int lane = threadIdx.x & 31;
     const int64_t first = blockIdx.x + int64_t(gridDim.x) * group, step = gridDim.x * int64_t(G);
     const int cols = static_cast<int>(p.cols), es = V::ES;
     const float inv = 1.0f / static_cast<float>(cols);
@@ -392,19 +409,13 @@ __global__ void __launch_bounds__(FWD_MAX_THREADS, 1) norm_fwd_kernel(const Norm
         if (T > 32) {
             const int W = T >> 5;
             float4* sc = scratch[buf] + group * W;
-            if ((threadIdx.x & 31) == 0) sc[tid >> 5] = make_float4(mean, q, n, 0.0f);
+            if (lane == 0) sc[tid >> 5] = make_float4(mean, q, n, 0.0f);
             group_sync(group, T);
-            if (!p.rms) {
-                float t = 0.0f;
-                for (int w = 0; w < W; ++w) t = fmaf(sc[w].x, sc[w].z, t);
-                mean = t * inv;
-            }
-            q = 0.0f;
-            for (int w = 0; w < W; ++w) {
-                const float4 e = sc[w];
-                const float d = e.x - mean;
-                q += fmaf(e.z * d, d, e.y);
-            }
+            // lane w of each half takes warp w's (at most 16 warps)
+            const float4 e = (lane & 15) < W ? sc[lane & 15] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!p.rms) mean = half_sum(e.x * e.z) * inv;
+            const float d = e.x - mean;
+            q = half_sum(fmaf(e.z * d, d, e.y));
             buf ^= 1;
         }
         const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
@@ -447,11 +458,12 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
 {
     using V = Vec<DT>;
     constexpr int N = V::N, P = V::P, S = BWD_STAGES<VPT>, MATS = RES ? 3 : 2;
-    __shared__ float2 scratch[2][BWD_MAX_THREADS / 32];
-    // ring [S][MATS][VPT][threads], then gamma [VPT * N / 4][T]; in the end G > 1: [2][cols] sums
+    __shared__ float scratch[2][2][BWD_MAX_THREADS / 32];
+    // ring [S][MATS][VPT][threads], then gamma [VPT * N / 4][T]; in the end the sums
     extern __shared__ uint4 stage_s[];
     int buf = 0;
     const int group = threadIdx.x / T, tid = threadIdx.x - group * T, G = blockDim.x / T, pitch = blockDim.x;
+    const int lane = threadIdx.x & 31;
     const int64_t first = blockIdx.x + int64_t(gridDim.x) * group, step = gridDim.x * int64_t(G);
     const int cols = static_cast<int>(p.cols), es = V::ES;
     const float inv = 1.0f / static_cast<float>(cols);
@@ -494,7 +506,8 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
     int st = 0;
     for (int64_t r = first; r < p.rows; r += step) {
         const float rstd = nrstd;
-        const u64 mean2 = pk2(nmean, nmean), rstd2 = pk2(rstd, rstd);
+        const float off = -nmean * rstd;   // xh = s rstd + off
+        const u64 off2 = pk2(off, off), rstd2 = pk2(rstd, rstd);
         ring.fetch(st == 0 ? S - 1 : st - 1, r + (S - 1) * step < p.rows, sp);
         if (r + step < p.rows) {
             if (!p.rms) nmean = __ldg(p.mean + r + step);
@@ -510,29 +523,25 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
             V::unpack(*ring.slot(st, 1, i), xh);
 #pragma unroll
             for (int j = 0; j < P; ++j) {   // (past the row's ends dy and gamma are 0)
-                xh[j] = mul2(sub2(xh[j], mean2), rstd2);
-                dg[i][j] = fma2(t[j], xh[j], dg[i][j]);
-                if (!p.rms) db[i][j] = add2(db[i][j], t[j]);
-                t[j] = mul2(t[j], g[j]);
-                a2 = add2(a2, t[j]);
-                b2 = fma2(t[j], xh[j], b2);
+                if (!p.rms) {
+                    db[i][j] = add2(db[i][j], t[j]);
+                    a2 = fma2(t[j], g[j], a2);
+                }
+                t[j] = mul2(t[j], fma2(xh[j], rstd2, off2));
+                dg[i][j] = add2(dg[i][j], t[j]);
+                b2 = fma2(t[j], g[j], b2);
             }
         }
-        float b = warp_sum(sum2(b2)), a = p.rms ? 0.0f : warp_sum(sum2(a2));
+        float v = warp_sum_ab(sum2(a2), sum2(b2), lane);   // lanes 0-15: a, lanes 16-31: b
         if (T > 32) {
-            const int W = T >> 5;
-            float2* sc = scratch[buf] + group * W;
-            if ((threadIdx.x & 31) == 0) sc[tid >> 5] = make_float2(a, b);
+            const int W = T >> 5, w0 = group * W, k = lane >> 4;
+            if ((lane & 15) == 0) scratch[buf][k][w0 + (tid >> 5)] = v;
             group_sync(group, T);
-            a = b = 0.0f;
-            for (int w = 0; w < W; ++w) {
-                const float2 e = sc[w];
-                a += e.x;
-                b += e.y;
-            }
+            v = half_sum((lane & 15) < W ? scratch[buf][k][w0 + (lane & 15)] : 0.0f);
             buf ^= 1;
         }
-        const float mt = a * inv, mtx = -(b * inv);
+        const float a = __shfl_sync(0xffffffffu, v, 0), b = __shfl_sync(0xffffffffu, v, 16);
+        const float mt = -(a * inv), mtx = -(b * inv);
         const u64 mt2 = pk2(mt, mt), mtx2 = pk2(mtx, mtx);
         uint8_t* at = dx + static_cast<int64_t>(sp.c0) * es;
 #pragma unroll
@@ -542,14 +551,15 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
             V::unpack(*ring.slot(st, 0, i), t);
             V::unpack(*ring.slot(st, 1, i), xh);
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                xh[j] = mul2(sub2(xh[j], mean2), rstd2);
-                t[j] = mul2(fma2(xh[j], mtx2, sub2(mul2(t[j], g[j]), mt2)), rstd2);
-            }
+            for (int j = 0; j < P; ++j)
+                t[j] = fma2(t[j], g[j], fma2(fma2(xh[j], rstd2, off2), mtx2, mt2));
             if constexpr (RES) {
                 V::unpack(*ring.slot(st, 2, i), xh);
 #pragma unroll
-                for (int j = 0; j < P; ++j) t[j] = add2(t[j], xh[j]);
+                for (int j = 0; j < P; ++j) t[j] = fma2(t[j], rstd2, xh[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < P; ++j) t[j] = mul2(t[j], rstd2);
             }
             const uint4 w = V::pack(t);
             st16(at + i * T * 16, w, sp.is_whole(i));
@@ -559,39 +569,35 @@ __global__ void __launch_bounds__(BWD_MAX_THREADS, 1) norm_bwd_kernel(const Norm
         st = st == S - 1 ? 0 : st + 1;
     }
     cp_wait<0>();
-    float* acc_s = reinterpret_cast<float*>(stage_s);
+    // the groups' sums meet in the ring's memory, each thread's in slots of its own; piece q of four columns is added
+    // over the groups, in order, by group q mod G
+    constexpr int PIECES = VPT * N / 4;
+    float4* acc_s = reinterpret_cast<float4*>(stage_s);
     __syncthreads();   // every row has been read
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+        const float2 a = up2(dg[4 * q / N][2 * q % P]), b = up2(dg[4 * q / N][2 * q % P + 1]);
+        acc_s[q * pitch + threadIdx.x] = make_float4(a.x, a.y, b.x, b.y);
+        const float2 c = up2(db[4 * q / N][2 * q % P]), d = up2(db[4 * q / N][2 * q % P + 1]);
+        acc_s[(PIECES + q) * pitch + threadIdx.x] = make_float4(c.x, c.y, d.x, d.y);
+    }
+    __syncthreads();
     float* part = p.part + 2LL * blockIdx.x * cols;
-    if (G > 1) {
-        for (int w = 0; w < G; ++w) {
-            if (group == w) {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const int c = sp.c0 + i * T * N + k;
-                        if (c >= 0 && c < cols) {
-                            const float2 vg = up2(dg[i][k / 2]), vb = up2(db[i][k / 2]);
-                            acc_s[c] = (w ? acc_s[c] : 0.0f) + (k & 1 ? vg.y : vg.x);
-                            acc_s[cols + c] = (w ? acc_s[cols + c] : 0.0f) + (k & 1 ? vb.y : vb.x);
-                        }
-                    }
-            }
-            __syncthreads();
+    for (int q = group; q < (p.dbeta ? 2 : 1) * PIECES; q += G) {
+        float4 v = acc_s[q * pitch + tid];
+        for (int w = 1; w < G; ++w) {
+            const float4 o = acc_s[q * pitch + w * T + tid];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
         }
-        for (int c = threadIdx.x; c < (p.dbeta ? 2 : 1) * cols; c += blockDim.x) part[c] = acc_s[c];
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int c = sp.c0 + i * T * N + k;
-                if (c >= 0 && c < cols) {
-                    const float2 vg = up2(dg[i][k / 2]), vb = up2(db[i][k / 2]);
-                    part[c] = k & 1 ? vg.y : vg.x;
-                    if (p.dbeta) part[cols + c] = k & 1 ? vb.y : vb.x;
-                }
-            }
+        const int h = q % PIECES, c = sp.c0 + h / (N / 4) * T * N + h % (N / 4) * 4;
+        float* out = part + (q < PIECES ? 0 : cols);
+        if (c >= 0 && c < cols) out[c] = v.x;
+        if (c + 1 >= 0 && c + 1 < cols) out[c + 1] = v.y;
+        if (c + 2 >= 0 && c + 2 < cols) out[c + 2] = v.z;
+        if (c + 3 >= 0 && c + 3 < cols) out[c + 3] = v.w;
     }
 }
 
@@ -601,11 +607,12 @@ struct RowPlan {
     int vpt, T, G;
 };
 
-// Two vectors a thread for the backward's registers (four beyond 1024
-// vectors), four for the forward wherever a row has them.
-inline bool row_plan(int64_t nv, bool bwd, int max_threads, RowPlan* q)
+// Four vectors a thread wherever a row has them: a row's reductions and its
+// barrier cost each thread the same for two (RMS backward, 8192 x 5120 bf16:
+// 77 us with two).
+inline bool row_plan(int64_t nv, int max_threads, RowPlan* q)
 {
-    q->vpt = (bwd ? nv <= 1024 : nv <= 64) ? 2 : 4;
+    q->vpt = nv <= 64 ? 2 : 4;
     const int64_t T = ((nv + q->vpt - 1) / q->vpt + 31) / 32 * 32;
     if (T > 512) return false;
     q->T = static_cast<int>(T);
@@ -639,7 +646,7 @@ cudaError_t launch_norm_fwd_1(const NormParams& p, const RowPlan& q, int sms, cu
 template <int DT, int VPT, bool FULL, bool RES>
 cudaError_t launch_norm_bwd_1(const NormBwdParams& p, const RowPlan& q, cudaStream_t stream)
 {
-    // the ring of rows holds the sums of both vectors afterwards: two floats for each element of a row's slots
+    // (the ring holds the sums afterwards: 8 bytes for each element of a row's slots, half of it with two matrices)
     NormBwdParams pp = p;
     const int ring = VPT * 16 * q.T * q.G * BWD_STAGES<VPT> * (RES ? 3 : 2), weights = VPT * 16 * q.T * (Vec<DT>::N / 4);
     pp.w_smem = ring + weights <= ROW_SMEM;
