@@ -69,7 +69,6 @@ constexpr int EPI_BUF = 4096;   // staging bytes of an epilogue warp: 32 rows x 
 constexpr int GEMM_A_BYTES = GEMM_BM * GEMM_BK * 2;
 constexpr int GEMM_STAGE = 2 * GEMM_A_BYTES;
 constexpr int GEMM_SMEM = GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * EPI_BUF + 1024;   // + slack to start on 1024 bytes
-constexpr int SPLIT_SMEM = GEMM_STAGES * GEMM_STAGE + 1024;
 
 // Columns that an epilogue warp stages at a time: rows of 128 bytes, or of 64
 // where its buffer holds two outputs.
@@ -111,13 +110,13 @@ __device__ __forceinline__ uint4 pack8(const float* v)
     return make_uint4(pack2(v[0], v[1], DT), pack2(v[2], v[3], DT), pack2(v[4], v[5], DT), pack2(v[6], v[7], DT));
 }
 
-// The 16-byte pieces at(0), at(1), ... of 32 elements of type dt.
-template <typename At>
-__device__ __forceinline__ void get32(int dt, float (&v)[32], At&& at)
+// W elements of type dt from the 16-byte pieces at(0), at(1), ..., and back.
+template <int W, typename At>
+__device__ __forceinline__ void get_row(int dt, float (&v)[W], At&& at)
 {
     if (dt == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < W / 4; ++i) {
             const uint4 w = *at(i);
             v[4 * i] = __uint_as_float(w.x);
             v[4 * i + 1] = __uint_as_float(w.y);
@@ -126,62 +125,71 @@ __device__ __forceinline__ void get32(int dt, float (&v)[32], At&& at)
         }
     } else if (dt == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unpack8<0>(*at(i), v + 8 * i);
+        for (int i = 0; i < W / 8; ++i) unpack8<0>(*at(i), v + 8 * i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unpack8<1>(*at(i), v + 8 * i);
+        for (int i = 0; i < W / 8; ++i) unpack8<1>(*at(i), v + 8 * i);
     }
 }
 
-template <typename At>
-__device__ __forceinline__ void put32(int dt, const float (&v)[32], At&& at)
+template <int W, typename At>
+__device__ __forceinline__ void put_row(int dt, const float (&v)[W], At&& at)
 {
     if (dt == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < W / 4; ++i)
             *at(i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
                                 __float_as_uint(v[4 * i + 3]));
     } else if (dt == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *at(i) = pack8<0>(v + 8 * i);
+        for (int i = 0; i < W / 8; ++i) *at(i) = pack8<0>(v + 8 * i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *at(i) = pack8<1>(v + 8 * i);
+        for (int i = 0; i < W / 8; ++i) *at(i) = pack8<1>(v + 8 * i);
     }
 }
 
-// 32 elements of one row from element `off` on, n of them in range.
-__device__ __forceinline__ void row_load32(const void* base, int64_t off, int dt, int n, float (&v)[32])
+// W elements of one row from element `off` on, n of them in range.
+template <int W>
+__device__ __forceinline__ void row_load(const void* base, int64_t off, int dt, int n, float (&v)[W])
 {
     const uint8_t* p = static_cast<const uint8_t*>(base) + off * dt_size(dt);
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        get32(dt, v, [&](int i) { return reinterpret_cast<const uint4*>(p) + i; });
+    if (n >= W && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        get_row<W>(dt, v, [&](int i) { return reinterpret_cast<const uint4*>(p) + i; });
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < n ? load_elem(p, i, dt) : 0.0f;
+        for (int i = 0; i < W; ++i) v[i] = i < n ? load_elem(p, i, dt) : 0.0f;
     }
 }
 
-__device__ __forceinline__ void row_store32(void* base, int64_t off, int dt, int n, const float (&v)[32])
+template <int W>
+__device__ __forceinline__ void row_store(void* base, int64_t off, int dt, int n, const float (&v)[W])
 {
     uint8_t* p = static_cast<uint8_t*>(base) + off * dt_size(dt);
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-        put32(dt, v, [&](int i) { return reinterpret_cast<uint4*>(p) + i; });
+    if (n >= W && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        put_row<W>(dt, v, [&](int i) { return reinterpret_cast<uint4*>(p) + i; });
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < W; ++i)
             if (i < n) store_elem(p, i, dt, v[i]);
     }
 }
 
-// Sum of each of 32 columns over the 32 lanes, in a fixed order: in step s a
-// lane keeps the half of its columns that its bit s selects and adds its
-// partner's copy of that half, so lane j ends with column j (31 shuffles
-// instead of 5 for each column).
-__device__ __forceinline__ float column_sum32(float (&v)[32], int lane)
+// Sum of each of W (32, 16 or 8) columns over the 32 lanes, in a fixed order:
+// in step s a lane keeps the half of its columns that its bit s selects and
+// adds its partner's copy of that half, so lane j < W ends with column j (31
+// shuffles for 32 columns instead of 160; with fewer columns, parts of the
+// warp are added first).
+template <int W>
+__device__ __forceinline__ float column_sum(float (&v)[W], int lane)
 {
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) {
+    for (int s = 16; s >= W; s >>= 1) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], s);
+    }
+#pragma unroll
+    for (int s = W / 2; s >= 1; s >>= 1) {
         const bool up = lane & s;
 #pragma unroll
         for (int i = 0; i < s; ++i) {
@@ -193,25 +201,25 @@ __device__ __forceinline__ float column_sum32(float (&v)[32], int lane)
     return v[0];
 }
 
-// The operator on 32 columns of a row: v (and u, the up projection's) hold the
+// The operator on W columns of a row: v (and u, the up projection's) hold the
 // accumulators, x aux where there is one; v (and u) leave as the outputs.
-template <int EPI, int NU>
-__device__ __forceinline__ void piece_math(const GemmParams& p, int col, int n, bool live, const float (&x)[32],
-                                           float (&v)[32], float (&u)[NU])
+template <int EPI, int W, int NU>
+__device__ __forceinline__ void piece_math(const GemmParams& p, int col, int n, bool live, const float (&x)[W],
+                                           float (&v)[W], float (&u)[NU])
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
     if constexpr (!DUAL) {
         if (p.bias) {
-            float b[32];
-            row_load32(p.bias, col, p.bias_dt, n, b);
+            float b[W];
+            row_load<W>(p.bias, col, p.bias_dt, n, b);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += b[i];
+            for (int i = 0; i < W; ++i) v[i] += b[i];
         }
     }
     with_act(p.act, [&](auto tag) {
         constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < W; ++i) {
             if constexpr (EPI == EPI_LINEAR) {
                 v[i] = act_value<ACT>(v[i]);
             } else if constexpr (EPI == EPI_GATED) {
@@ -231,16 +239,17 @@ __device__ __forceinline__ void piece_math(const GemmParams& p, int col, int n, 
     if constexpr (EPI == EPI_LINEAR) {
         if (p.aux) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += x[i];
+            for (int i = 0; i < W; ++i) v[i] += x[i];
         }
     }
 }
 
 // Column sums of dz over the 32 rows from row0 on.
-__device__ __forceinline__ void piece_colsum(const GemmParams& p, int row0, int col, int n, int lane, float (&v)[32])
+template <int W>
+__device__ __forceinline__ void piece_colsum(const GemmParams& p, int row0, int col, int n, int lane, float (&v)[W])
 {
-    const float sum = column_sum32(v, lane);
-    if (lane < n) p.colsum[static_cast<int64_t>(row0 / 32) * p.N + col + lane] = sum;
+    const float sum = column_sum<W>(v, lane);
+    if (lane < W && lane < n) p.colsum[static_cast<int64_t>(row0 / 32) * p.N + col + lane] = sum;
 }
 
 template <bool A_MN, bool B_MN, int EPI>
@@ -259,6 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
+        prefetch_map(&p.a[0]);
+        prefetch_map(&p.b[0]);
         for (int i = 0; i < GEMM_STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -449,23 +460,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                             aux_ph ^= 1u;
                             if (!ok) break;
                         }
-                        get32(p.aux_dt, x, [&](int i) { return at(buf, c, i); });
+                        get_row<32>(p.aux_dt, x, [&](int i) { return at(buf, c, i); });
                     } else if (live) {
-                        row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
+                        row_load<32>(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
                     }
                 }
                 if (some) {
-                    piece_math<EPI>(p, col, n, live, x, v, u);
+                    piece_math<EPI, 32>(p, col, n, live, x, v, u);
                     if (p.staged) {
-                        put32(p.out_dt, v, [&](int i) { return at(buf, c, i); });
-                        if constexpr (EPI == EPI_GATED_BWD) put32(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
+                        put_row<32>(p.out_dt, v, [&](int i) { return at(buf, c, i); });
+                        if constexpr (EPI == EPI_GATED_BWD) put_row<32>(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
                     } else if (live) {
-                        row_store32(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
+                        row_store<32>(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
                         if constexpr (EPI == EPI_GATED_BWD)
-                            row_store32(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
+                            row_store<32>(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
                     }
                     if constexpr (EPI == EPI_LINEAR_BWD) {
-                        if (p.colsum) piece_colsum(p, row0, col, n, lane, v);
+                        if (p.colsum) piece_colsum<32>(p, row0, col, n, lane, v);
                     }
                 }
                 if (p.staged && ((c + 32) & (box - 1)) == 0) {
@@ -494,18 +505,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
 
 // ---------------------------------------------------------------- split kernel
 // Products whose 128 x 128 tiles do not fill the GPU: a cluster of S CTAs
-// computes one tile, each a part of the contraction, and the parts meet in
-// shared memory: every CTA writes its accumulators there (FP32), and each
-// piece of 32 rows x 32 columns is summed in rank order by one warp of the
-// cluster, which runs the epilogue on it.  Nothing passes through HBM and one
-// launch does it.
-__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank)
+// computes one tile, each a part of the contraction.  Each CTA finishes a
+// slice of the tile's columns: every CTA writes its FP32 accumulators to
+// shared memory slice by slice, sends each slice to its CTA in one bulk copy
+// (shared memory to shared memory, complete on a barrier there), and adds what
+// it receives in rank order.  Nothing passes through HBM and one launch does
+// it.  (Loads from the other CTAs' shared memory instead were bound by their
+// latency: 22 us for 1024 x 4096 x 256 tokens with S = 8.)
+constexpr int SPLIT_STAGES = 5;
+constexpr int SPLIT_ACC = GEMM_BM * 128 * 4;   // a tile's accumulators
+constexpr int SPLIT_SMEM = SPLIT_STAGES * GEMM_STAGE + SPLIT_ACC + 1024;
+
+// Byte of 16-byte piece `k` of row `row` in a slice with rows of `bytes` (64 or
+// more): pieces are permuted so that 8 rows' accesses to one piece cover all banks.
+__device__ __forceinline__ uint32_t slice_at(int row, int k, int bytes)
 {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
+    return row * bytes + ((k ^ (bytes == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+}
+
+__device__ __forceinline__ void bulk_send(void* dst, const void* src, int bytes, uint64_t* bar, int rank)
+{
+    uint32_t d, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(dst)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(d),
+                 "r"(smem_u32(src)), "r"(bytes), "r"(b)
+                 : "memory");
+}
+
+// A piece of W columns of 32 rows, finished and stored.  `load(c, v)` gives
+// the accumulators of the lane's row from column c of the tile on (the gated
+// forms: of G; `load_u` of U).
+template <int EPI, int W, typename Load, typename LoadU>
+__device__ __forceinline__ void split_piece(const GemmParams& p, int g, int row0, int col, int lane, Load&& load,
+                                            LoadU&& load_u)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+    const int row = row0 + lane, n = p.N - col;
+    const bool live = row < p.M;
+    const int64_t row64 = row;
+    float x[W], v[W], u[DUAL ? W : 1];
+    if (p.aux && live) row_load<W>(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
+    load(v);
+    if constexpr (DUAL) load_u(u);
+    piece_math<EPI, W>(p, col, n, live, x, v, u);
+    if (live) {
+        row_store<W>(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
+        if constexpr (EPI == EPI_GATED_BWD) row_store<W>(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
+    }
+    if constexpr (EPI == EPI_LINEAR_BWD) {
+        if (p.colsum) piece_colsum<W>(p, row0, col, n, lane, v);
+    }
+}
+
+// The pieces of this CTA's slice: `own` is its own part, `received` +
+// k * slice_bytes that of CTA k.
+template <int EPI, int W>
+__device__ __forceinline__ void split_pieces(const GemmParams& p, const uint8_t* own, const uint8_t* received, int rank,
+                                             int g, int m0, int n0, int warp, int lane)
+{
+    constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+    const int S = p.split, row_bytes = 128 * 4 / S, slice_bytes = GEMM_BM * row_bytes;
+    const int cols = (DUAL ? 64 : 128) / S;   // output columns of the slice
+#pragma unroll 1
+    for (int u0 = warp; u0 < 4 * (cols / W); u0 += GEMM_EPI_WARPS) {
+        const int q = u0 & 3, c = (u0 >> 2) * W, col = n0 + rank * cols + c, row0 = m0 + 32 * q;
+        if (col >= p.N || row0 >= p.M) continue;
+        auto from = [&](int c1, float (&v)[W]) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = 0.0f;
+#pragma unroll 2
+            for (int k = 0; k < S; ++k) {
+                const uint8_t* src = k == rank ? own : received + k * slice_bytes;
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const float4 t = *reinterpret_cast<const float4*>(src + slice_at(32 * q + lane, c1 / 4 + i, row_bytes));
+                    v[4 * i] += t.x;
+                    v[4 * i + 1] += t.y;
+                    v[4 * i + 2] += t.z;
+                    v[4 * i + 3] += t.w;
+                }
+            }
+        };
+        split_piece<EPI, W>(p, g, row0, col, lane, [&](float (&v)[W]) { from(c, v); },
+                            [&](auto& u) { if constexpr (DUAL) from(cols + c, u); });
+    }
 }
 
 template <bool A_MN, bool B_MN, int EPI>
@@ -514,7 +598,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
     constexpr int BN = 128, TILE_N = DUAL ? BN / 2 : BN;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[GEMM_STAGES], empty[GEMM_STAGES], acc_full;
+    __shared__ uint64_t full[SPLIT_STAGES], empty[SPLIT_STAGES], acc_full, recv_full;
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
@@ -530,19 +614,28 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.nk) * rank / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.nk) * (rank + 1) / S);
 
+    if (threadIdx.x == 64) {
+        prefetch_map(&p.a[0]);
+        prefetch_map(&p.b[0]);
+    }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < GEMM_STAGES; ++i) {
+        for (int i = 0; i < SPLIT_STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(&acc_full, 1);
+        mbar_init(&recv_full, 1);
         failed = 0;
         fence_barrier_init();
+        if (S > 1) mbar_arrive_expect_tx(&recv_full, SPLIT_ACC / S * (S - 1));
     }
     __syncwarp();
     if (warp == 1) tmem_alloc<1>(&tmem_slot, BN);
     tc_fence_before();
-    __syncthreads();
+    if (S > 1)
+        cluster_sync();   // the barriers exist before another CTA's slice completes on them
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
@@ -553,8 +646,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             bool ok = true;
             int done = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++done) {
-                const int s = done % GEMM_STAGES;
-                if (done >= GEMM_STAGES && !mbar_wait(&empty[s], (done / GEMM_STAGES - 1) & 1, p.err)) {
+                const int s = done % SPLIT_STAGES;
+                if (done >= SPLIT_STAGES && !mbar_wait(&empty[s], (done / SPLIT_STAGES - 1) & 1, p.err)) {
                     ok = false;
                     break;
                 }
@@ -584,16 +677,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             if (!ok) {   // let the loads in flight land before the shared memory goes away
                 failed = 1;
                 const uint64_t until = globaltimer_ns() + 2000000000ull;
-                for (int j = done > GEMM_STAGES ? done - GEMM_STAGES : 0; j < done; ++j)
-                    mbar_wait_until(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1, until);
+                for (int j = done > SPLIT_STAGES ? done - SPLIT_STAGES : 0; j < done; ++j)
+                    mbar_wait_until(&full[j % SPLIT_STAGES], (j / SPLIT_STAGES) & 1, until);
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
             bool ok = true;
             for (int i = 0; i < kb1 - kb0; ++i) {
-                const int s = i % GEMM_STAGES;
-                if (!mbar_wait(&full[s], (i / GEMM_STAGES) & 1, p.err)) {
+                const int s = i % SPLIT_STAGES;
+                if (!mbar_wait(&full[s], (i / SPLIT_STAGES) & 1, p.err)) {
                     ok = false;
                     break;
                 }
@@ -613,60 +706,77 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
         }
     }
     __syncwarp();
-    // accumulators to shared memory, [column][row], over the operand ring (every product has read it by now)
-    float* acc_s = reinterpret_cast<float*>(smem);
     if (warp >= 2) {
         const int q = warp & 3, half = (warp - 2) >> 2;
         if (!mbar_wait(&acc_full, 0, p.err)) failed = 1;
         tc_fence_after();
         __syncwarp();
-        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-            float v[32];
-            tmem_ld32(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
-            tmem_ld_wait();
+        const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        if (S == 1) {   // the whole sum is here
+#pragma unroll 1
+            for (int c = half * (TILE_N / 2); c < (half + 1) * (TILE_N / 2) && !failed; c += 32) {
+                float v[32], u[DUAL ? 32 : 1];
+                tmem_ld32(acc + c, v);
+                if constexpr (DUAL) tmem_ld32(acc + TILE_N + c, u);
+                tmem_ld_wait();
+                if (n0 + c >= p.N || m0 + 32 * q >= p.M) continue;
+                split_piece<EPI, 32>(
+                    p, g, m0 + 32 * q, n0 + c, lane,
+                    [&](float (&w)[32]) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc_s[(c + i) * GEMM_BM + 32 * q + lane] = v[i];
+                        for (int i = 0; i < 32; ++i) w[i] = v[i];
+                    },
+                    [&](auto& w) {
+                        if constexpr (DUAL) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) w[i] = u[i];
+                        }
+                    });
+            }
+            tc_fence_before();
+        } else {
+            // accumulators to shared memory by slices, over the operand ring (every product has read it by now)
+            const int row_bytes = BN * 4 / S, slice_bytes = GEMM_BM * row_bytes;
+            const int ls = S == 2 ? 1 : S == 4 ? 2 : 3;
+            uint8_t* received = smem + SPLIT_STAGES * GEMM_STAGE;
+#pragma unroll 1
+            for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
+                float v[32];
+                tmem_ld32(acc + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // the gated forms' slice: its columns of G, then the same of U
+                    const int j = (c0 + 4 * i) & (TILE_N - 1), width = TILE_N >> ls;
+                    const int slice = j >> ((DUAL ? 6 : 7) - ls), at = (j & (width - 1)) + (c0 >= TILE_N ? width : 0);
+                    *reinterpret_cast<float4*>(smem + slice * slice_bytes + slice_at(32 * q + lane, at / 4, row_bytes)) =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * GEMM_EPI_WARPS) : "memory");
+            if (warp == 2 && lane < S && lane != rank && !failed)
+                bulk_send(received + rank * slice_bytes, smem + lane * slice_bytes, slice_bytes, &recv_full, lane);
+            __syncwarp();
+            if (!mbar_wait(&recv_full, 0, p.err)) failed = 1;
+            __syncwarp();
+            cluster_arrive();   // (all of this CTA's slices that anyone waits for have come)
+            if (!failed) {
+                const uint8_t* own = smem + rank * slice_bytes;
+                if (TILE_N / S >= 16)
+                    split_pieces<EPI, 16>(p, own, received, rank, g, m0, n0, warp - 2, lane);
+                else
+                    split_pieces<EPI, 8>(p, own, received, rank, g, m0, n0, warp - 2, lane);
+            }
         }
-        tc_fence_before();
+    } else if (S > 1) {
+        cluster_arrive();
     }
     __syncwarp();
-    cluster_sync();
-    if (warp >= 2 && !failed) {
-        constexpr int PIECES = 4 * (TILE_N / 32);
-        for (int u0 = rank + S * (warp - 2); u0 < PIECES; u0 += S * GEMM_EPI_WARPS) {
-            const int q = u0 & 3, c = (u0 >> 2) * 32;
-            const int col = n0 + c, row0 = m0 + 32 * q, row = row0 + lane, n = p.N - col;
-            if (n <= 0 || row0 >= p.M) continue;
-            const bool live = row < p.M;
-            const int64_t row64 = row;
-            float x[32], v[32], u[DUAL ? 32 : 1];
-            if (p.aux && live) row_load32(p.aux, row64 * p.ld_aux + col, p.aux_dt, n, x);
-            const uint32_t at = smem_u32(acc_s + c * GEMM_BM + 32 * q + lane);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ld_cluster(at + i * GEMM_BM * 4, 0);
-            for (int k = 1; k < S; ++k)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += ld_cluster(at + i * GEMM_BM * 4, k);
-            if constexpr (DUAL) {
-                const uint32_t up = at + TILE_N * GEMM_BM * 4;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = ld_cluster(up + i * GEMM_BM * 4, 0);
-                for (int k = 1; k < S; ++k)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) u[i] += ld_cluster(up + i * GEMM_BM * 4, k);
-            }
-            piece_math<EPI>(p, col, n, live, x, v, u);
-            if (live) {
-                row_store32(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
-                if constexpr (EPI == EPI_GATED_BWD) row_store32(p.out[1], row64 * p.ld_out[1] + col, p.out_dt, n, u);
-            }
-            if constexpr (EPI == EPI_LINEAR_BWD) {
-                if (p.colsum) piece_colsum(p, row0, col, n, lane, v);
-            }
-        }
-    }
-    __syncwarp();
-    cluster_sync();   // the others have read this CTA's accumulators
+    if (S > 1) cluster_wait();   // the others have received this CTA's slices
+    __syncthreads();
+    tc_fence_after();
     if (warp == 1) tmem_dealloc<1>(tmem, BN);
 }
 

@@ -116,6 +116,10 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same in two steps, without ordering memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // Address of `p` (shared memory of this CTA) in the even CTA of the pair.
 __device__ __forceinline__ uint32_t leader_addr(const void* p)
 {
@@ -161,6 +165,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         " [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
+}
+
+// Fetches a tensor map (a kernel parameter) ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // 32 lanes (rows) x 32 columns of FP32 accumulators: column j in v[j].
