@@ -3,23 +3,24 @@
 
 namespace qta {
 
-// Pairs where more than half of them find a 256 x 256 tile, else the split
-// kernel: its 128 x 128 tiles, at most as many as SMs, with the contraction of
-// each split until the GPU is full (2, 4 or 8 CTAs; each keeps at least
-// MIN_SPLIT_BLOCKS blocks, below which the join costs more than the split
-// gains).
-constexpr int MIN_SPLIT_BLOCKS = 3;
+// Pairs of CTAs on 256 x 256 tiles where the 128 x 128 tiles are more than the
+// SMs, else the split kernel on those (1021 x 1000 -> 1096, bf16: 9 us against
+// 22 in 20 pairs).  The contraction of each is split while SMs are left (of
+// `sms`, or of half of them where two such launches run side by side) and a
+// CTA keeps at least 4 blocks; the join takes as long as 8 blocks, so
+// contractions below 20 blocks stay whole (17 blocks: 8.9 us split in two, 8.6
+// whole).
+constexpr int SPLIT_MIN_BLOCKS = 20;
 
-GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms)
+GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared)
 {
-    (void)form;
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const int64_t pair_n = dual ? 128 : 256, pairs = ((M + 255) / 256) * ((N + pair_n - 1) / pair_n) * groups;
     const int64_t tile_n = dual ? 64 : 128, tiles = ((M + 127) / 128) * ((N + tile_n - 1) / tile_n) * groups;
-    if (tiles > sms) return {256, static_cast<int>(pair_n), 128, 0};
-    (void)pairs;
+    if (tiles > sms) return {256, dual ? 128 : 256, 128, 0};
+    const int64_t room = shared ? sms / 2 : sms;
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= sms && blocks >= 2 * s * MIN_SPLIT_BLOCKS) s *= 2;
+    if (blocks >= SPLIT_MIN_BLOCKS)
+        while (s < 8 && tiles * s * 2 <= room && blocks >= 8 * s) s *= 2;
     return {128, static_cast<int>(tile_n), static_cast<int>(tile_n), s};
 }
 

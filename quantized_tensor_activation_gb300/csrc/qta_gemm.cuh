@@ -54,6 +54,11 @@ struct GemmParams {
     int staged;
     CUtensorMap aux_map, out_map[2];
     int split;                  // CTAs that share a tile's contraction (split kernel)
+    // The launch reads nothing that the launch before it on the stream writes,
+    // and what it does read was complete when that one began: it starts beside
+    // it (filling the SMs that its last tiles leave idle) and waits for it at
+    // its own end instead, so that whatever follows still follows both.
+    int beside;
     unsigned int* err;
 };
 
@@ -267,19 +272,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     const int rank = static_cast<int>(cluster_rank());
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 64) {
         prefetch_map(&p.a[0]);
         prefetch_map(&p.b[0]);
-        for (int i = 0; i < GEMM_STAGES; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+    }
+    if (warp == 0) {
+        if (lane < GEMM_STAGES) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
+        } else if (lane < GEMM_STAGES + 2) {
+            mbar_init(&acc_full[lane - GEMM_STAGES], 1);
+            mbar_init(&acc_empty[lane - GEMM_STAGES], GEMM_EPI_WARPS * 2);
+        } else if (lane < GEMM_STAGES + 2 + GEMM_EPI_WARPS) {
+            mbar_init(&aux_full[lane - GEMM_STAGES - 2], 1);
+        } else if (lane == 31) {
+            mbar_init(&drain, 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], GEMM_EPI_WARPS * 2);
-        }
-        for (int i = 0; i < GEMM_EPI_WARPS; ++i) mbar_init(&aux_full[i], 1);
-        mbar_init(&drain, 1);
         fence_barrier_init();
     }
     __syncwarp();
@@ -288,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     cluster_sync();   // the barriers of both CTAs exist before either signals the other
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();
+    if (!p.beside) pdl_wait();
     // after the allocation: a successor that starts early allocates only once this CTA has what it needs
     pdl_trigger();
 
@@ -501,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     cluster_sync();
     tc_fence_after();
     if (warp == 1) tmem_dealloc<2>(tmem, 2 * BN);
+    if (p.beside) pdl_wait();
 }
 
 // ---------------------------------------------------------------- split kernel
@@ -618,16 +627,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
         prefetch_map(&p.a[0]);
         prefetch_map(&p.b[0]);
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < SPLIT_STAGES; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+    const int live = min(GEMM_BM, p.M - m0);   // rows of the tile in range
+    if (warp == 0) {
+        if (lane < SPLIT_STAGES) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
+        } else if (lane == 30) {
+            mbar_init(&acc_full, 1);
+            failed = 0;
+        } else if (lane == 31) {
+            mbar_init(&recv_full, 1);
         }
-        mbar_init(&acc_full, 1);
-        mbar_init(&recv_full, 1);
-        failed = 0;
         fence_barrier_init();
-        if (S > 1) mbar_arrive_expect_tx(&recv_full, SPLIT_ACC / S * (S - 1));
+        if (lane == 31 && S > 1) mbar_arrive_expect_tx(&recv_full, live * (BN * 4 / S) * (S - 1));
     }
     __syncwarp();
     if (warp == 1) tmem_alloc<1>(&tmem_slot, BN);
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();
+    if (!p.beside) pdl_wait();
     pdl_trigger();
 
     if (warp == 0) {
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             fence_proxy_async_smem();
             asm volatile("bar.sync 1, %0;" ::"n"(32 * GEMM_EPI_WARPS) : "memory");
             if (warp == 2 && lane < S && lane != rank && !failed)
-                bulk_send(received + rank * slice_bytes, smem + lane * slice_bytes, slice_bytes, &recv_full, lane);
+                bulk_send(received + rank * slice_bytes, smem + lane * slice_bytes, live * row_bytes, &recv_full, lane);
             __syncwarp();
             if (!mbar_wait(&recv_full, 0, p.err)) failed = 1;
             __syncwarp();
@@ -778,6 +790,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc<1>(tmem, BN);
+    if (p.beside) pdl_wait();
 }
 
 }  // namespace qta

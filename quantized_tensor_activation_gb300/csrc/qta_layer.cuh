@@ -26,7 +26,7 @@ enum GemmForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 struct GemmTile {
     int rows, cols, b_box, split;
 };
-GemmTile gemm_tile(int form, int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms);
+GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared);
 cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
 
 // Products of up to SKINNY_ROWS tokens (qta_skinny.cu).

@@ -171,18 +171,27 @@ bool tma_ok(const View& v)
     return reinterpret_cast<uintptr_t>(v.p) % 16 == 0 && (v.ld * v.es) % 16 == 0 && (v.cols * v.es) % 16 == 0;
 }
 
+// Where a launch stands among those of its call: after what it reads, or beside
+// the launch before it (GemmParams::beside); `shared`: a product of its kind
+// runs beside it.
+struct Place {
+    bool beside, shared;
+};
+constexpr Place ALONE = {false, false};
+
 // One launch: D[M, N] over contraction K of a[0] and b[0] (and of a[1], b[1]
 // where given: `groups` == 1 adds their product to the same D, 2 computes a
 // second D of a[1] and b[0]).  The epilogue fields of p are the caller's.
 qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt, const View* a0, const View* a1, const View* b0,
-                    const View* b1, int64_t M, int64_t N, int64_t K, int groups, cudaStream_t s)
+                    const View* b1, int64_t M, int64_t N, int64_t K, int groups, Place place, cudaStream_t s)
 {
     int sms = 0;
     if (query_device(&sms, &p.err) != cudaSuccess) return QTA_ERR_CUDA;
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
     p.nk0 = p.nk = static_cast<int>(ceil_div(K, GEMM_BK));
     if (a1 && groups == 1 && !dual) p.nk *= 2;
-    const GemmTile t = gemm_tile(form, epi, M, N, p.nk, groups, sms);
+    const GemmTile t = gemm_tile(epi, M, N, p.nk, groups, sms, place.shared);
+    p.beside = place.beside;
     p.split = t.split;
     const int a_rows = form == FORM_TN ? 64 : GEMM_BM;
     const int b_rows = form == FORM_NT ? t.b_box : 64;
@@ -417,7 +426,7 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     p.bias_dt = d->bias_dtype;
     p.out_dt = d->out_dtype;
     return run_gemm(FORM_NT, EPI_LINEAR, p, {&vy, nullptr, residual ? &vr : nullptr}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
-                    reinterpret_cast<cudaStream_t>(stream));
+                    ALONE, reinterpret_cast<cudaStream_t>(stream));
 }
 
 // Row partitions of dbias: one per 32 rows where the epilogue sums dz,
@@ -475,7 +484,7 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
         p.out_dt = d->dtype;
         p.colsum = dbias ? part : nullptr;
         st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, {&dz, nullptr, &vdy}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
-                      cs);
+                      ALONE, cs);
         if (st != QTA_OK) return st;
     }
     if (dbias) {
@@ -488,13 +497,15 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1, cs);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1,
+                      {dbias != nullptr, dw != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     if (dw) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdw, nullptr, nullptr}, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1, cs);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdw, nullptr, nullptr}, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1,
+                      {dx || dbias, dx != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     return QTA_OK;
@@ -523,7 +534,7 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     p.act = d->act;
     p.out_dt = d->dtype;
     return run_gemm(FORM_NT, EPI_GATED, p, {&vh, nullptr, nullptr}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
-                    reinterpret_cast<cudaStream_t>(stream));
+                    ALONE, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t qta_gated_ffn_bwd_workspace_bytes(const qta_ffn_desc* d)
@@ -566,19 +577,22 @@ qta_status qta_gated_ffn_bwd(const qta_ffn_desc* d, const qta_mat* dh, const qta
         GemmParams p = blank();
         p.act = d->act;
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, {&mg, &mu, &vdh}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1, cs);
+        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, {&mg, &mu, &vdh}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
+                      ALONE, cs);
         if (st != QTA_OK) return st;
     }
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1, cs);
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1,
+                      {false, dwg != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     if (dwg) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdg, &vdu, nullptr}, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2, cs);
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdg, &vdu, nullptr}, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2,
+                      {dx != nullptr, dx != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     return QTA_OK;
