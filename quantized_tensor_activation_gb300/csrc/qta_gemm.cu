@@ -7,10 +7,10 @@ namespace qta {
 // SMs, else the split kernel on those (1021 x 1000 -> 1096, bf16: 9 us against
 // 22 in 20 pairs).  The contraction of each is split while SMs are left (of
 // `sms`, or of half of them where two such launches run side by side) and a
-// CTA keeps at least 4 blocks; the join takes as long as 8 blocks, so
-// contractions below 20 blocks stay whole (17 blocks: 8.9 us split in two, 8.6
-// whole).
-constexpr int SPLIT_MIN_BLOCKS = 20;
+// CTA keeps at least 4 blocks: a block takes 0.30 us, the join as long as 5 to
+// 8 of them (512 x 1024, S = 1, 2, 4: 16 blocks 9.8, 8.2, 8.1 us; 8 blocks 7.1,
+// 6.5, 7.2 us; 1021 x 1096: 16 blocks 9.9, 8.9 us; 8 blocks 7.2, 7.4 us).
+constexpr int SPLIT_MIN_BLOCKS = 12;
 
 GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared)
 {
@@ -20,7 +20,7 @@ GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, in
     const int64_t room = shared ? sms / 2 : sms;
     int s = 1;
     if (blocks >= SPLIT_MIN_BLOCKS)
-        while (s < 8 && tiles * s * 2 <= room && blocks >= 8 * s) s *= 2;
+        while (s < 8 && tiles * s * 2 <= room && blocks >= 4 * (2 * s)) s *= 2;
     return {128, static_cast<int>(tile_n), static_cast<int>(tile_n), s};
 }
 

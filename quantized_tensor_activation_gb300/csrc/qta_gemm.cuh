@@ -154,16 +154,34 @@ __device__ __forceinline__ void put_row(int dt, const float (&v)[W], At&& at)
     }
 }
 
-// W elements of one row from element `off` on, n of them in range.
+// W elements of one row from element `off` on, n of them in range: 16 bytes at
+// a time where the row is aligned, the elements of a last, partial piece singly.
 template <int W>
 __device__ __forceinline__ void row_load(const void* base, int64_t off, int dt, int n, float (&v)[W])
 {
     const uint8_t* p = static_cast<const uint8_t*>(base) + off * dt_size(dt);
-    if (n >= W && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (vec && n >= W) {
         get_row<W>(dt, v, [&](int i) { return reinterpret_cast<const uint4*>(p) + i; });
     } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = i < n ? load_elem(p, i, dt) : 0.0f;
+        for (int i = 0; i < W; ++i) v[i] = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < W && i < n; i += 8) {
+            float t[8];
+            if (vec && i + 8 <= n) {
+                get_row<8>(dt, t, [&](int j) { return reinterpret_cast<const uint4*>(p + i * dt_size(dt)) + j; });
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] = i + j < n ? load_elem(p, i + j, dt) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < W; k += 8)
+                if (k == i) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[k + j] = t[j];
+                }
+        }
     }
 }
 
@@ -171,12 +189,27 @@ template <int W>
 __device__ __forceinline__ void row_store(void* base, int64_t off, int dt, int n, const float (&v)[W])
 {
     uint8_t* p = static_cast<uint8_t*>(base) + off * dt_size(dt);
-    if (n >= W && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const bool vec = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (vec && n >= W) {
         put_row<W>(dt, v, [&](int i) { return reinterpret_cast<uint4*>(p) + i; });
     } else {
+#pragma unroll 1
+        for (int i = 0; i < W && i < n; i += 8) {
+            float t[8];
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (i < n) store_elem(p, i, dt, v[i]);
+            for (int k = 0; k < W; k += 8)
+                if (k == i) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) t[j] = v[k + j];
+                }
+            if (vec && i + 8 <= n) {
+                put_row<8>(dt, t, [&](int j) { return reinterpret_cast<uint4*>(p + i * dt_size(dt)) + j; });
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (i + j < n) store_elem(p, i + j, dt, t[j]);
+            }
+        }
     }
 }
 
@@ -502,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();   // the last boxes have left this CTA's shared memory
+        if (lane == 0) bulk_wait_read<0>();   // the last boxes have left this CTA's shared memory
     }
     __syncwarp();
     tc_fence_before();
