@@ -38,15 +38,33 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int dt)
 
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU_TANH = 3, ACT_GELU_ERF = 4 };
 
-// 1 / (1 + e^-z) by the fast exponential and division: their errors (a few
-// ulp of FP32) are far below half an ulp of the 16-bit types the result is
-// rounded to.  e^-z = inf for z < -88.7 gives 0.
-__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
-// GELU's tanh form is z sigmoid(2 q) with q = sqrt(2/pi) (z + 0.044715 z^3).
-__device__ __forceinline__ float gelu_tanh_2q(float z)
+__device__ __forceinline__ float ex2_fast(float x)
 {
-    return z * fmaf(0.0713548162726009f, z * z, 1.5957691216057308f);
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + 2^t), the logistic function of -t ln 2, by the hardware's
+// approximate exponential and reciprocal: their errors (a few ulp of FP32) are
+// far below half an ulp of the 16-bit types the result is rounded to.  2^t =
+// inf gives 0; values below 2^-126 become 0.
+__device__ __forceinline__ float logistic2(float t) { return rcp_fast(1.0f + ex2_fast(t)); }
+
+__device__ __forceinline__ float sigmoid_fast(float z) { return logistic2(-1.4426950408889634f * z); }
+
+// GELU's tanh form is z sigmoid(2 q), q = sqrt(2/pi) (z + 0.044715 z^3); this
+// is sigmoid(2 q).
+__device__ __forceinline__ float gelu_tanh_gate(float z)
+{
+    return logistic2(z * fmaf(-0.1029432395800235f, z * z, -2.302208198144325f));
 }
 
 template <int ACT>
@@ -54,7 +72,7 @@ __device__ __forceinline__ float act_value(float z)
 {
     if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
     if constexpr (ACT == ACT_SILU) return z * sigmoid_fast(z);
-    if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid_fast(gelu_tanh_2q(z));
+    if constexpr (ACT == ACT_GELU_TANH) return z * gelu_tanh_gate(z);
     if constexpr (ACT == ACT_GELU_ERF) return 0.5f * z * erfcf(-0.7071067811865476f * z);   // no cancellation for z << 0
     return z;
 }
@@ -73,7 +91,7 @@ __device__ __forceinline__ void act_both(float z, float& f, float& df)
         f = z * p;
         df = fmaf(f, 1.0f - p, p);
     } else if constexpr (ACT == ACT_GELU_TANH) {
-        const float p = sigmoid_fast(gelu_tanh_2q(z));
+        const float p = gelu_tanh_gate(z);
         f = z * p;
         df = fmaf(f * (1.0f - p), fmaf(0.2140644488178027f, z * z, 1.5957691216057308f), p);
     } else if constexpr (ACT == ACT_GELU_ERF) {

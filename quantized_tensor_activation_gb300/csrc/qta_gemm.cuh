@@ -64,16 +64,16 @@ struct GemmParams {
 
 constexpr int GEMM_BM = 128;   // rows of one CTA's share of a tile
 constexpr int GEMM_BK = 64;
-constexpr int GEMM_STAGES = 6;
+constexpr int GEMM_STAGES = 5;
 constexpr int GEMM_EPI_WARPS = 8;
 constexpr int GEMM_THREADS = 64 + 32 * GEMM_EPI_WARPS;
-constexpr int EPI_BUF = 4096;   // staging bytes of an epilogue warp: 32 rows x 128 bytes
+constexpr int EPI_BUF = 4096;   // a staging buffer of an epilogue warp: 32 rows x 128 bytes; each warp has two
 
 // A stage holds 128 rows of A and 128 of B: the pair's tile is 256 x 256, each
 // CTA with its half of both; the split kernel's 128 x 128.
 constexpr int GEMM_A_BYTES = GEMM_BM * GEMM_BK * 2;
 constexpr int GEMM_STAGE = 2 * GEMM_A_BYTES;
-constexpr int GEMM_SMEM = GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * EPI_BUF + 1024;   // + slack to start on 1024 bytes
+constexpr int GEMM_SMEM = GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * 2 * EPI_BUF + 1024;   // + slack to start on 1024 bytes
 
 // Columns that an epilogue warp stages at a time: rows of 128 bytes, or of 64
 // where its buffer holds two outputs.
@@ -297,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     constexpr int BN = 256, TILE_N = DUAL ? BN / 2 : BN;   // accumulator and output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[GEMM_STAGES], empty[GEMM_STAGES], acc_full[2], acc_empty[2], drain;
-    __shared__ uint64_t aux_full[GEMM_EPI_WARPS];
+    __shared__ uint64_t aux_full[GEMM_EPI_WARPS * 2];
     __shared__ uint32_t tmem_slot;
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -316,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
         } else if (lane < GEMM_STAGES + 2) {
             mbar_init(&acc_full[lane - GEMM_STAGES], 1);
             mbar_init(&acc_empty[lane - GEMM_STAGES], GEMM_EPI_WARPS * 2);
-        } else if (lane < GEMM_STAGES + 2 + GEMM_EPI_WARPS) {
+        } else if (lane < GEMM_STAGES + 2 + 2 * GEMM_EPI_WARPS) {
             mbar_init(&aux_full[lane - GEMM_STAGES - 2], 1);
         } else if (lane == 31) {
             mbar_init(&drain, 1);
@@ -433,21 +433,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
         }
     } else {
         // Epilogue warps: each has 32 rows (the TMEM lanes its index mod 4 may
-        // read) and half of the tile's columns, in pieces of 32.  Staged, aux
-        // arrives in the warp's buffer by TMA (the first box before the
+        // read) and half of the tile's columns, in pieces of 32.  Staged, the
+        // columns pass in boxes of one or two pieces through the warp's two
+        // buffers: aux arrives there by TMA (the first two boxes before the
         // accumulators are ready), each lane replaces its own row by the
         // output, and the box leaves by TMA: full lines, and a quarter of the
-        // shared-memory and L1 cycles of 16-byte accesses to 32 rows, which
-        // the operand ring needs.
+        // shared-memory and L1 cycles of 16-byte accesses to 32 rows.
         constexpr int HALF = TILE_N / 2;
         const int q = warp & 3, ew = warp - 2, half = ew >> 2;
         const bool f32 = p.out_dt == 2;
         const int box = epi_box_cols(EPI, f32);
         const int row_bytes = (f32 || box == 64) ? 128 : 64;
         const uint32_t box_bytes = 32u * row_bytes;
-        uint8_t* buf = smem + GEMM_STAGES * GEMM_STAGE + ew * EPI_BUF;
-        uint8_t* buf2 = buf + EPI_BUF / 2;   // EPI_GATED_BWD: the second output
-        uint32_t aux_ph = 0;
+        uint8_t* const bufs = smem + GEMM_STAGES * GEMM_STAGE + ew * 2 * EPI_BUF;
+        uint32_t aux_ph = 0;   // bit b: phase of buffer b's barrier
         int it = 0;
         bool ok = true;   // after an expired wait a warp goes on without work
         for (int t = first; t < n_tiles; t += step, ++it) {
@@ -459,36 +458,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
             const int row = row0 + lane;
             const bool live = row < p.M;
             const int64_t row64 = row;
-            // the warp's buffer is free again; aux of the columns from c on
-            auto refill = [&](int c) {
-                if (lane == 0) {
-                    bulk_wait_read<0>();
-                    if (p.aux && row0 < p.M && n0 + c < p.N) {
-                        mbar_arrive_expect_tx(&aux_full[ew], box_bytes);
-                        tma_load_2d(buf, &p.aux_map, n0 + c, row0, &aux_full[ew]);
-                    }
+            // box b of the tile (columns b * box ...) uses buffer b & 1
+            auto fetch_aux = [&](int b) {
+                if (p.aux && b * box < HALF && row0 < p.M && n0 + b * box < p.N) {
+                    uint64_t* bar = &aux_full[2 * ew + (b & 1)];
+                    mbar_arrive_expect_tx(bar, box_bytes);
+                    tma_load_2d(bufs + (b & 1) * EPI_BUF, &p.aux_map, n0 + b * box, row0, bar);
                 }
-                __syncwarp();
             };
             // 16-byte piece i of this lane's row, for the 32 columns from c on
             auto at = [&](uint8_t* b, int c, int i) {
                 const uint32_t k = static_cast<uint32_t>(i) + (row_bytes == 128 && !f32 && (c & 32) ? 4u : 0u);
                 return reinterpret_cast<uint4*>(b + (row_bytes == 128 ? sw128(lane, k) : sw64(lane, k)));
             };
-            if (p.staged && ok) refill(0);   // (an aux box lands within the two seconds of an expired wait)
+            if (p.staged && ok) {   // (an aux box lands within the two seconds of an expired wait)
+                if (lane == 0) {
+                    bulk_wait_read<0>();
+                    fetch_aux(0);
+                    fetch_aux(1);
+                }
+                __syncwarp();
+            }
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (it >> 1) & 1, p.err));
             tc_fence_after();
             const uint32_t acc = tmem + ab * BN + half * HALF + (static_cast<uint32_t>(32 * q) << 16);
+            float nv[32];   // the accumulators of the next piece (the gated forms have no registers for them)
+            if constexpr (!DUAL) tmem_ld32(acc, nv);
 #pragma unroll 1
             for (int c = 0; ok && c < HALF; c += 32) {
                 const int col = n0 + c;
                 const int n = p.N - col;   // columns in range (may be <= 0)
                 const bool some = n > 0 && row0 < p.M;
+                const int b = c / box;
+                uint8_t* buf = bufs + (b & 1) * EPI_BUF;
+                uint8_t* buf2 = buf + EPI_BUF / 2;   // EPI_GATED_BWD: the second output
                 float v[32], u[DUAL ? 32 : 1];
-                tmem_ld32(acc + c, v);
-                if constexpr (DUAL) tmem_ld32(acc + TILE_N + c, u);
-                tmem_ld_wait();
-                if (c + 32 >= HALF) {   // the accumulators have been read
+                if constexpr (DUAL) {
+                    tmem_ld32(acc + c, v);
+                    tmem_ld32(acc + TILE_N + c, u);
+                    tmem_ld_wait(v);
+                    tmem_ld_wait(u);
+                } else {
+                    tmem_ld_wait(nv);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = nv[i];
+                }
+                if (c + 32 < HALF) {
+                    if constexpr (!DUAL) tmem_ld32(acc + c + 32, nv);
+                } else {   // the accumulators have been read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(leader_addr(&acc_empty[ab]));
@@ -497,8 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                 if (p.aux && some) {
                     if (p.staged) {
                         if ((c & (box - 1)) == 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(&aux_full[ew], aux_ph, p.err));
-                            aux_ph ^= 1u;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&aux_full[2 * ew + (b & 1)], (aux_ph >> (b & 1)) & 1u, p.err));
+                            aux_ph ^= 1u << (b & 1);
                             if (!ok) break;
                         }
                         get_row<32>(p.aux_dt, x, [&](int i) { return at(buf, c, i); });
@@ -521,17 +538,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                     }
                 }
                 if (p.staged && ((c + 32) & (box - 1)) == 0) {
-                    if (n > 32 - box && row0 < p.M) {   // the box has columns in range
+                    const bool out = n > 32 - box && row0 < p.M;   // the box has columns in range
+                    if (out) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                    }
+                    if (lane == 0) {
+                        if (out) {
                             const int c0 = col + 32 - box;
                             tma_store_2d(&p.out_map[g], c0, row0, buf);
                             if constexpr (EPI == EPI_GATED_BWD) tma_store_2d(&p.out_map[1], c0, row0, buf2);
                             bulk_commit();
                         }
+                        if ((b + 2) * box < HALF) {   // this buffer again
+                            bulk_wait_read<0>();
+                            fetch_aux(b + 2);
+                        }
                     }
-                    if (c + 32 < HALF) refill(c + 32);
+                    __syncwarp();
                 }
             }
         }
@@ -539,7 +563,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    cluster_arrive();   // (nothing in memory is ordered by it: neither CTA frees what the other still uses)
+    cluster_wait();
     tc_fence_after();
     if (warp == 1) tmem_dealloc<2>(tmem, 2 * BN);
     if (p.beside) pdl_wait();
@@ -762,8 +787,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             for (int c = half * (TILE_N / 2); c < (half + 1) * (TILE_N / 2) && !failed; c += 32) {
                 float v[32], u[DUAL ? 32 : 1];
                 tmem_ld32(acc + c, v);
-                if constexpr (DUAL) tmem_ld32(acc + TILE_N + c, u);
-                tmem_ld_wait();
+                if constexpr (DUAL) {
+                    tmem_ld32(acc + TILE_N + c, u);
+                    tmem_ld_wait(u);
+                }
+                tmem_ld_wait(v);
                 if (n0 + c >= p.N || m0 + 32 * q >= p.M) continue;
                 split_piece<EPI, 32>(
                     p, g, m0 + 32 * q, n0 + c, lane,
@@ -788,7 +816,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
                 float v[32];
                 tmem_ld32(acc + c0, v);
-                tmem_ld_wait();
+                tmem_ld_wait(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     // the gated forms' slice: its columns of G, then the same of U

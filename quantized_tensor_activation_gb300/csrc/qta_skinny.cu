@@ -68,11 +68,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // NT: tokens in groups of 8.  DUAL: the gated form.
+//
+// Each warp keeps the loads of U steps in flight (of the two weights' rows in
+// the gated form).  Four CTAs on an SM hold 8192 x 3584's 512 at once, 11.8 us
+// for one token; three leave a second wave, 13.6 us.  The gated form does best
+// with two CTAs and four steps: 5120 -> 3456, 6 tokens 13.6 us, against 14.5
+// with three and two.
 template <int DT, int NT, bool DUAL>
-__global__ void __launch_bounds__(32 * SK_WARPS, NT == 1 ? 3 : 2) skinny_kernel(const SkinnyParams p)
+__global__ void __launch_bounds__(32 * SK_WARPS, NT == 1 && !DUAL ? 4 : 2) skinny_kernel(const SkinnyParams p)
 {
     constexpr int W = DUAL ? 2 : 1;
-    constexpr int U = DUAL ? 2 : 4;   // steps whose loads are in flight together
+    constexpr int U = DUAL && NT == 2 ? 2 : 4;
     __shared__ float part[SK_WARPS][W][8 * NT][SK_ROWS + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = blockIdx.x * SK_ROWS;

@@ -128,9 +128,12 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p)
     return r;
 }
 
+// Arrival on a barrier of the pair's even CTA.  What it hands over is TMEM,
+// ordered by the tcgen05 fences; ordering memory as well would wait for every
+// store in flight (1000 cycles in an epilogue).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // mbar_wait for arrivals from the other CTA of the pair (cluster scope).
@@ -188,6 +191,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32])
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this warp's TMEM loads; v passes through it, so that nothing uses
+// the values before.
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+                 "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+                 "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
 
 }  // namespace qta
