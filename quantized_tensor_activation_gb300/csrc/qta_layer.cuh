@@ -29,8 +29,11 @@ struct GemmTile {
 GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared);
 cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
 
-// Products of up to SKINNY_ROWS tokens (qta_skinny.cu).
-constexpr int64_t SKINNY_ROWS = 16;
+// Whether qta_skinny.cu takes a forward product: up to 16 tokens, and up to 32
+// where the contraction is short (n_in, tokens: its time against the split
+// kernel's; 1024, 32: 7.2 and 8.4 us; 2048, 32: 6.9 and 8.2; 3584, 32: 18.8 and
+// 15.2; 4096, 17: 9.1 and 7.4).
+inline bool skinny(int64_t rows, int64_t n_in) { return rows <= 16 || (rows <= 32 && n_in <= 2048); }
 
 struct SkinnyParams {
     const uint8_t* x;

@@ -417,7 +417,7 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     o.output(vy);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
-    if (d->rows <= SKINNY_ROWS)
+    if (skinny(d->rows, d->n_in))
         return run_skinny(d->dtype, vx, vw, nullptr, bias, d->bias_dtype, residual ? &vr : nullptr, vy, d->out_dtype,
                           d->act, reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();
@@ -527,7 +527,7 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     o.output(vh);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
-    if (d->rows <= SKINNY_ROWS)
+    if (skinny(d->rows, d->hidden))
         return run_skinny(d->dtype, vx, vg, &vu, nullptr, 0, nullptr, vh, d->dtype, d->act,
                           reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();

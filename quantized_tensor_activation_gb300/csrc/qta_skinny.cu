@@ -1,5 +1,5 @@
 // qta_skinny.cu -- products of few tokens: y = f(x w^T + b) + r and the gated
-// block for up to 16 rows of x, where reading the weights once is all that
+// block for up to 32 rows of x, where reading the weights once is all that
 // counts (2 M operations per 2-byte weight: HBM-bound up to M of several
 // hundred, while a tcgen05 tile would be 7/8 empty and its ring one CTA deep).
 //
@@ -78,7 +78,7 @@ template <int DT, int NT, bool DUAL>
 __global__ void __launch_bounds__(32 * SK_WARPS, NT == 1 && !DUAL ? 4 : 2) skinny_kernel(const SkinnyParams p)
 {
     constexpr int W = DUAL ? 2 : 1;
-    constexpr int U = DUAL && NT == 2 ? 2 : 4;
+    constexpr int U = NT == 4 || (DUAL && NT == 2) ? 2 : 4;
     __shared__ float part[SK_WARPS][W][8 * NT][SK_ROWS + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = blockIdx.x * SK_ROWS;
@@ -152,36 +152,37 @@ __global__ void __launch_bounds__(32 * SK_WARPS, NT == 1 && !DUAL ? 4 : 2) skinn
             part[warp][i][8 * j + 2 * t + 1][g + 8] = c[i][j][3];
         }
     __syncthreads();
-    const int e = threadIdx.x, row = e & (SK_ROWS - 1), m = e / SK_ROWS, n = n0 + row;   // 256 threads: 16 x 16
-    if (m >= p.M || n >= p.N) return;
-    float v[W];
+    const int row = threadIdx.x & (SK_ROWS - 1), n = n0 + row;
+    if (n >= p.N) return;
+    for (int m = threadIdx.x / SK_ROWS; m < p.M; m += 32 * SK_WARPS / SK_ROWS) {
+        float v[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        v[i] = part[0][i][m][row];
+        for (int i = 0; i < W; ++i) {
+            v[i] = part[0][i][m][row];
 #pragma unroll
-        for (int w = 1; w < SK_WARPS; ++w) v[i] += part[w][i][m][row];
+            for (int w = 1; w < SK_WARPS; ++w) v[i] += part[w][i][m][row];
+        }
+        if (p.bias) v[0] += load_elem(p.bias, n, p.bias_dt);
+        with_act(p.act, [&](auto tag) { v[0] = act_value<decltype(tag)::value>(v[0]); });
+        if constexpr (DUAL) v[0] *= v[1];
+        if (p.aux) v[0] += load_elem(p.aux, m * p.ld_aux + n, p.out_dt);
+        store_elem(p.out, m * p.ld_out + n, p.out_dt, v[0]);
     }
-    if (p.bias) v[0] += load_elem(p.bias, n, p.bias_dt);
-    with_act(p.act, [&](auto tag) { v[0] = act_value<decltype(tag)::value>(v[0]); });
-    if constexpr (DUAL) v[0] *= v[1];
-    if (p.aux) v[0] += load_elem(p.aux, m * p.ld_aux + n, p.out_dt);
-    store_elem(p.out, m * p.ld_out + n, p.out_dt, v[0]);
 }
 
-template <int DT>
-static cudaError_t launch_s(bool dual, const SkinnyParams& p, cudaStream_t stream)
+template <int DT, bool DUAL>
+static cudaError_t launch_s(const SkinnyParams& p, cudaStream_t stream)
 {
     const dim3 grid((p.N + SK_ROWS - 1) / SK_ROWS), block(32 * SK_WARPS);
-    if (dual)
-        return p.M <= 8 ? launch_pdl(skinny_kernel<DT, 1, true>, grid, block, 0, stream, p)
-                        : launch_pdl(skinny_kernel<DT, 2, true>, grid, block, 0, stream, p);
-    return p.M <= 8 ? launch_pdl(skinny_kernel<DT, 1, false>, grid, block, 0, stream, p)
-                    : launch_pdl(skinny_kernel<DT, 2, false>, grid, block, 0, stream, p);
+    if (p.M <= 8) return launch_pdl(skinny_kernel<DT, 1, DUAL>, grid, block, 0, stream, p);
+    if (p.M <= 16) return launch_pdl(skinny_kernel<DT, 2, DUAL>, grid, block, 0, stream, p);
+    return launch_pdl(skinny_kernel<DT, 4, DUAL>, grid, block, 0, stream, p);
 }
 
 cudaError_t launch_skinny(int dt, bool dual, const SkinnyParams& p, cudaStream_t stream)
 {
-    return dt == 0 ? launch_s<0>(dual, p, stream) : launch_s<1>(dual, p, stream);
+    if (dual) return dt == 0 ? launch_s<0, true>(p, stream) : launch_s<1, true>(p, stream);
+    return dt == 0 ? launch_s<0, false>(p, stream) : launch_s<1, false>(p, stream);
 }
 
 }  // namespace qta
