@@ -1,0 +1,172 @@
+"""A tensor-parallel feed-forward layer of n simulated ranks, forward and
+backward, with both of its all-reduces through the codec: the place where the
+layer operators and the codec meet (TACO: the compressed tensors are the
+row-parallel outputs of TP layers and the gradients of their inputs; Flash
+Communication: the two-step all-reduce after the down projection).
+
+Forward, for input x and residual stream r (rank i holds a slice of the
+feed-forward width):
+    s   = x + r,  y = norm(s) gamma + beta                      qta_norm
+    h_i = f(y wg_i^T) * (y wu_i^T)                              qta_gated_ffn
+    p_i = h_i wd_i^T (rank 0 adds the bias)                     qta_linear
+    o   = decompress(reduce + requantize(compress(p_i)))        the codec
+Backward, for do (gradient of o) and ds (gradient that reaches s elsewhere):
+    dh_i, dwd_i (dbias)    from do                              qta_linear_bwd
+    dy_i, dwg_i, dwu_i     from dh_i                            qta_gated_ffn_bwd
+    dy  = the same all-reduce of dy_i                           the codec
+    dx, dgamma (dbeta)     from dy, ds                          qta_norm_bwd
+
+The object owns the buffers of one (rows, hidden, widths) shape and reuses
+them from step to step; every arithmetic step is a call of the C ABI.
+
+    python -m quantized_tensor_activation_gb300.tp_ffn      # a step, timed
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (BF16, FP16, SCALE_CURRENT, alloc_qtensor, desc, qar_reduce_requant, taco_compress, taco_decompress)
+from .layer import (alloc_workspace, ffn_desc, gated_ffn_bwd_workspace_bytes, linear_bwd_workspace_bytes, linear_desc,
+                    norm_bwd_workspace_bytes, norm_desc, qta_gated_ffn, qta_gated_ffn_bwd, qta_linear, qta_linear_bwd,
+                    qta_norm, qta_norm_bwd)
+
+_DT = {"bf16": (BF16, torch.bfloat16), "fp16": (FP16, torch.float16)}
+# reduce-stage scheme -> (its block, gather-stage scheme, its block)
+CODECS = {"taco_fp8": (128, "taco_fp8", 128), "int8_sym": (64, "int8_sym", 64), "int4_asym": (128, "int8_asym", 128)}
+
+
+class AllReduce:
+    """The two-step all-reduce of n ranks' [rows, cols] tensors through the codec: compress, reduce + requantize,
+    decompress."""
+
+    def __init__(self, n: int, rows: int, cols: int, dtype: str, codec: str = "taco_fp8", device="cuda"):
+        if codec not in CODECS:
+            raise ValueError(f"codec {codec!r}: one of {sorted(CODECS)}")
+        block, gather, gather_block = CODECS[codec]
+        if cols % max(block, gather_block):
+            raise ValueError(f"{cols} channels: a multiple of {max(block, gather_block)} is needed by {codec}")
+        self.dt = _DT[dtype][0]
+        self.rows = rows
+        self.d_all = desc(codec, block, rows, cols, batch=n)
+        self.d_one = desc(codec, block, rows, cols)
+        # each rank requantizes its own shard of the rows, with its own scale, where the rows divide
+        shards = n if rows % n == 0 else 1
+        self.d_out = desc(gather, gather_block, rows // shards, cols, batch=shards)
+        self.q = alloc_qtensor(self.d_all, device)
+        self.g = alloc_qtensor(self.d_out, device)
+        self.shards = [self.q.shard(i) for i in range(n)]
+
+    def __call__(self, parts, out, stream=None) -> None:
+        """parts: [n, rows, cols], contiguous; out: [rows, cols]."""
+        taco_compress(self.d_all, parts, self.dt, self.q, SCALE_CURRENT, stream)
+        qar_reduce_requant(self.d_one, self.shards, 0, self.rows, self.d_out, self.g, SCALE_CURRENT, stream)
+        taco_decompress(self.d_out, self.g, out, self.dt, stream)
+
+
+class TPFeedForward:
+    """widths: each rank's share of the feed-forward width.  Parameters travel as a dict: gamma [hidden], beta
+    (layer norm) or None, wg, wu (lists of [width_i, hidden]), wd (list of [hidden, width_i]), bias [hidden] or
+    None."""
+
+    def __init__(self, rows: int, hidden: int, widths, dtype: str = "bf16", kind: str = "rms", act: str = "silu",
+                 eps: float = 1e-5, codec: str = "taco_fp8", device="cuda"):
+        self.rows, self.hidden, self.widths, self.kind = rows, hidden, list(widths), kind
+        n, td = len(self.widths), _DT[dtype][1]
+        self.nd = norm_desc(rows, hidden, dtype, kind, eps)
+        self.fd = [ffn_desc(rows, hidden, w, dtype, act) for w in self.widths]
+        self.ld = [linear_desc(rows, hidden, w, dtype) for w in self.widths]
+        self.all_reduce = AllReduce(n, rows, hidden, dtype, codec, device)
+
+        def new(*shape, dtype=td):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.s, self.y, self.o = new(rows, hidden), new(rows, hidden), new(rows, hidden)
+        self.mean = new(rows, dtype=torch.float32) if kind == "layer" else None
+        self.rstd = new(rows, dtype=torch.float32)
+        self.h = [new(rows, w) for w in self.widths]
+        self.parts = new(n, rows, hidden)   # the ranks' partial outputs, then the partial gradients of y
+        self.dh = [new(rows, w) for w in self.widths]
+        self.dy, self.dx = new(rows, hidden), new(rows, hidden)
+        need = [norm_bwd_workspace_bytes(self.nd)] + [linear_bwd_workspace_bytes(d) for d in self.ld] + \
+               [gated_ffn_bwd_workspace_bytes(d) for d in self.fd]
+        self.ws = alloc_workspace(max(need), device)
+
+    def forward(self, x, p, residual=None, stream=None):
+        """Returns (s, o): the new residual stream and the layer's output (what the next norm adds to s).  Both,
+        and what the backward pass needs, stay in this object's buffers."""
+        qta_norm(self.nd, x, p["gamma"], self.y, beta=p.get("beta"), residual=residual, sum_out=self.s, mean=self.mean,
+                 rstd=self.rstd, stream=stream)
+        for i in range(len(self.widths)):
+            qta_gated_ffn(self.fd[i], self.y, p["wg"][i], p["wu"][i], self.h[i], stream=stream)
+            qta_linear(self.ld[i], self.h[i], p["wd"][i], self.parts[i], bias=p.get("bias") if i == 0 else None,
+                       stream=stream)
+        self.all_reduce(self.parts, self.o, stream)
+        return self.s, self.o
+
+    def backward(self, do, p, ds=None, stream=None):
+        """Gradients after forward(): (dx, grads), dx that of x and of residual alike, grads a dict like p."""
+        like = torch.empty_like
+        f32 = dict(dtype=torch.float32, device=do.device)
+        g = {"wg": [like(w) for w in p["wg"]], "wu": [like(w) for w in p["wu"]], "wd": [like(w) for w in p["wd"]],
+             "gamma": torch.empty(self.hidden, **f32), "beta": None, "bias": None}
+        if p.get("beta") is not None:
+            g["beta"] = torch.empty(self.hidden, **f32)
+        if p.get("bias") is not None:
+            g["bias"] = torch.empty(self.hidden, **f32)
+        for i in range(len(self.widths)):
+            qta_linear_bwd(self.ld[i], do, self.h[i], p["wd"][i], self.dh[i], g["wd"][i], self.ws,
+                           dbias=g["bias"] if i == 0 else None, stream=stream)
+            qta_gated_ffn_bwd(self.fd[i], self.dh[i], self.y, p["wg"][i], p["wu"][i], self.parts[i], g["wg"][i],
+                              g["wu"][i], self.ws, stream=stream)
+        self.all_reduce(self.parts, self.dy, stream)
+        qta_norm_bwd(self.nd, self.dy, self.s, p["gamma"], self.rstd, self.dx, g["gamma"], self.ws, mean=self.mean,
+                     dbeta=g["beta"], dsum=ds, stream=stream)
+        return self.dx, g
+
+
+def random_params(hidden: int, widths, dtype: str = "bf16", kind: str = "rms", bias: bool = False, seed: int = 0,
+                  device="cuda"):
+    """Parameters of a layer with unit-scale outputs."""
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    td, total = _DT[dtype][1], sum(widths)
+
+    def normal(*shape, std):
+        return (torch.randn(shape, generator=gen, device=device) * std).to(td)
+
+    return {"gamma": 1 + normal(hidden, std=0.1), "beta": normal(hidden, std=0.1) if kind == "layer" else None,
+            "wg": [normal(w, hidden, std=hidden ** -0.5) for w in widths],
+            "wu": [normal(w, hidden, std=hidden ** -0.5) for w in widths],
+            "wd": [normal(hidden, w, std=total ** -0.5) for w in widths],
+            "bias": normal(hidden, std=0.1) if bias else None}
+
+
+def main() -> None:
+    """One training step of a layer, 4 ranks, 8192 tokens x 5120 channels, 3456 of the width each; timed on the
+    device after warm-up."""
+    rows, hidden, widths = 8192, 5120, [3456] * 4
+    p = random_params(hidden, widths)
+    layer = TPFeedForward(rows, hidden, widths)
+    x, r, do, ds = (torch.randn(rows, hidden, device="cuda").bfloat16() for _ in range(4))
+
+    def step():
+        layer.forward(x, p, residual=r)
+        layer.backward(do, p, ds=ds)
+
+    for _ in range(3):
+        step()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    begin.record()
+    for _ in range(10):
+        step()
+    end.record()
+    torch.cuda.synchronize()
+    ms = begin.elapsed_time(end) / 10
+    flop = rows * hidden * sum(widths) * (4 + 2 + 4 + 12)
+    print(f"{len(widths)} ranks, {rows} x {hidden}, width {sum(widths)}: {ms:.2f} ms a step (forward + backward, both "
+          f"all-reduces), {flop / ms / 1e9:.0f} TFLOP/s of products")
+
+
+if __name__ == "__main__":
+    main()
