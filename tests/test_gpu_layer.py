@@ -206,7 +206,10 @@ def test_norm_bwd(dev, R, C, kind, dt):
 LIN_SHAPES = [  # rows, n_out, n_in
     (1, 8, 8), (1, 129, 64), (2, 64, 72), (3, 1000, 200), (6, 264, 520), (8, 8, 1096), (9, 128, 128), (16, 256, 64),
     (17, 200, 136), (31, 72, 2056), (33, 65, 64), (64, 128, 192), (127, 129, 264), (128, 128, 64), (129, 384, 72),
-    (300, 344, 1024), (257, 513, 328), (1, 4096, 4096), (5, 2048, 4104), (1000, 40, 40)]
+    (300, 344, 1024), (257, 513, 328), (1, 4096, 4096), (5, 2048, 4104), (1000, 40, 40),
+    # more 128 x 128 tiles than SMs: pairs of CTAs, several tiles each, ragged ends, one contraction block, one column block
+    (1700, 1800, 1504), (1701, 1801, 1496), (2049, 2312, 520), (5000, 600, 8), (20001, 8, 64), (24, 136, 2048),
+    (32, 1000, 2056)]
 ACTS = ["none", "relu", "silu", "gelu_tanh", "gelu_erf"]
 
 
@@ -286,7 +289,8 @@ def test_linear_bwd(dev, R, N, K, dt, gdt):
 # ---------------------------------------------------------------- gated feed-forward
 FFN_SHAPES = [  # rows, hidden, width
     (1, 8, 8), (1, 520, 65), (2, 72, 64), (6, 5120, 3456), (9, 64, 136), (16, 256, 264), (17, 1000, 72), (40, 136, 200),
-    (128, 64, 64), (129, 328, 130), (300, 1024, 344), (1, 4096, 1024)]
+    (128, 64, 64), (129, 328, 130), (300, 1024, 344), (1, 4096, 1024), (24, 512, 1000), (32, 2056, 72),
+    (1300, 1904, 904), (1281, 2000, 901), (10001, 64, 72)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
