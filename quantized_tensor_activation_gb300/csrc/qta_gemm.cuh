@@ -54,6 +54,7 @@ struct GemmParams {
     int staged;
     CUtensorMap aux_map, out_map[2];
     int split;                  // CTAs that share a tile's contraction (split kernel)
+    int stage_bytes;            // what TMA writes of a stage (split kernel: boxes hold no rows past M and N)
     // The launch reads nothing that the launch before it on the stream writes,
     // and what it does read was complete when that one began: it starts beside
     // it (filling the SMs that its last tiles leave idle) and waits for it at
@@ -571,6 +572,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
 }
 
 // ---------------------------------------------------------------- split kernel
+// (Rows of a tile past M or N: where one box holds the operand's 128 rows it is
+// cut to what exists, and the products of the rows below it, of whatever the
+// stage held, go to accumulators that nothing reads.)
+//
 // Products whose 128 x 128 tiles do not fill the GPU: a cluster of S CTAs
 // computes one tile, each a part of the contraction.  Each CTA finishes a
 // slice of the tile's columns: every CTA writes its FP32 accumulators to
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
                 const CUtensorMap* mb = &p.b[second];
                 uint8_t* sa = smem + s * GEMM_STAGE;
                 uint8_t* sb = sa + GEMM_A_BYTES;
-                mbar_arrive_expect_tx(&full[s], GEMM_STAGE);
+                mbar_arrive_expect_tx(&full[s], p.stage_bytes);
                 if constexpr (A_MN) {
                     tma_load_2d(sa, ma, m0, k0, &full[s]);
                     tma_load_2d(sa + BOX_BYTES, ma, m0 + 64, k0, &full[s]);

@@ -193,8 +193,13 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
     const GemmTile t = gemm_tile(epi, M, N, p.nk, groups, sms, place.shared);
     p.beside = place.beside;
     p.split = t.split;
-    const int a_rows = form == FORM_TN ? 64 : GEMM_BM;
-    const int b_rows = form == FORM_NT ? t.b_box : 64;
+    int a_rows = form == FORM_TN ? 64 : GEMM_BM, b_rows = form == FORM_NT ? t.b_box : 64;
+    if (t.split) {   // no more rows than there are, in groups of 8 (the swizzle's)
+        const int a_boxes = form == FORM_TN ? 2 : 1, b_boxes = form == FORM_NT ? (dual ? 2 : 1) : 2;
+        if (form != FORM_TN && M < a_rows) a_rows = static_cast<int>(round_up(M, 8));
+        if (form == FORM_NT && N < b_rows) b_rows = static_cast<int>(round_up(N, 8));
+        p.stage_bytes = (a_rows * a_boxes + b_rows * b_boxes) * GEMM_BK * 2;
+    }
     if (!map_mat(&p.a[0], *a0, a_rows) || !map_mat(&p.b[0], *b0, b_rows)) return QTA_ERR_CUDA;
     if (a1 && !map_mat(&p.a[1], *a1, a_rows)) return QTA_ERR_CUDA;
     if (b1 && !map_mat(&p.b[1], *b1, b_rows)) return QTA_ERR_CUDA;
