@@ -4,15 +4,28 @@
 //
 // with an epilogue that finishes the operator in registers.  A pair of CTAs
 // computes tiles of 256 x 256: warp 0 loads A and B in blocks of 64
-// contraction elements by TMA into a ring of shared-memory stages, warp
-// 1 issues tcgen05.mma on them, warps 2-9 read the accumulators of the
-// previous tile (TMEM holds two) and run the epilogue.  In a pair each CTA
-// loads and keeps half of B, so a byte of shared memory feeds twice the
-// products that it feeds in a single CTA, whose 128 x 128 tile is bound by
-// shared memory (8192 x 8192 -> 3584 gated, fp16: 1004 us in single CTAs, 644
-// in pairs).  Products too small for the pairs run the split kernel below.  Operands whose contraction index is
-// not the contiguous one (the backward products) are read as they lie, with
-// MN-major descriptors: nothing is transposed in memory.
+// contraction elements by TMA into a ring of shared-memory stages, warp 1
+// issues tcgen05.mma on them, warps 2-9 read the accumulators of the previous
+// tile (TMEM holds two) and run the epilogue.  In a pair each CTA loads and
+// keeps half of B, so a byte of shared memory feeds twice the products that it
+// feeds in a single CTA, whose 128 x 128 tile is bound by shared memory (8192 x
+// 8192 -> 3584 gated, fp16: 1004 us in single CTAs, 629 in pairs).  Products
+// too small for the pairs run the split kernel below.
+//
+// Operands whose contraction index is not the contiguous one (the backward
+// products) are read as they lie, with MN-major descriptors: nothing is
+// transposed in memory, and all three forms run at one rate.
+//
+// What bounds the pairs is the tensor cores: a block of a tile takes 605 cycles
+// with and without its loads (2170 TFLOP/s at 2.06 GHz).  Large products run at
+// the power limit (1.5 to 1.9 GHz): 8192^3 bf16 602 us, 1827 TFLOP/s, in bursts
+// of 20; 8192 x 8192 x 7168 fp16 1525 TFLOP/s for seconds on end.  The rest is
+// the last, partial round of tiles, the first loads (4000 cycles when they
+// come from HBM) and the last epilogue (5000 to 9000 cycles).
+//
+// Accumulation on the tensor cores is FP32 that truncates: a sum over K terms
+// comes out small by about K 1e-9 of itself (K = 4096: 4e-6; rounded FP32 sums
+// are off by 6e-7 there).
 //
 // Rows and columns past an operand's end are filled with zeros by TMA, and
 // contraction elements past its end too, so ragged sizes need no other path.
@@ -74,7 +87,8 @@ constexpr int EPI_BUF = 4096;   // a staging buffer of an epilogue warp: 32 rows
 // CTA with its half of both; the split kernel's 128 x 128.
 constexpr int GEMM_A_BYTES = GEMM_BM * GEMM_BK * 2;
 constexpr int GEMM_STAGE = 2 * GEMM_A_BYTES;
-constexpr int GEMM_SMEM = GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * 2 * EPI_BUF + 1024;   // + slack to start on 1024 bytes
+constexpr int GEMM_SMEM =   // with slack to start on 1024 bytes
+    GEMM_STAGES * GEMM_STAGE + GEMM_EPI_WARPS * 2 * EPI_BUF + 1024;
 
 // Columns that an epilogue warp stages at a time: rows of 128 bytes, or of 64
 // where its buffer holds two outputs.
@@ -292,7 +306,8 @@ __device__ __forceinline__ void piece_colsum(const GemmParams& p, int row0, int 
 }
 
 template <bool A_MN, bool B_MN, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
+    gemm_kernel(const __grid_constant__ GemmParams p)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
     constexpr int BN = 256, TILE_N = DUAL ? BN / 2 : BN;   // accumulator and output columns of a tile
@@ -515,7 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                 if (p.aux && some) {
                     if (p.staged) {
                         if ((c & (box - 1)) == 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(&aux_full[2 * ew + (b & 1)], (aux_ph >> (b & 1)) & 1u, p.err));
+                            const uint32_t ph = (aux_ph >> (b & 1)) & 1u;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&aux_full[2 * ew + (b & 1)], ph, p.err));
                             aux_ph ^= 1u << (b & 1);
                             if (!ok) break;
                         }
@@ -528,7 +544,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
                     piece_math<EPI, 32>(p, col, n, live, x, v, u);
                     if (p.staged) {
                         put_row<32>(p.out_dt, v, [&](int i) { return at(buf, c, i); });
-                        if constexpr (EPI == EPI_GATED_BWD) put_row<32>(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
+                        if constexpr (EPI == EPI_GATED_BWD)
+                            put_row<32>(p.out_dt, u, [&](int i) { return at(buf2, c, i); });
                     } else if (live) {
                         row_store<32>(p.out[g], row64 * p.ld_out[g] + col, p.out_dt, n, v);
                         if constexpr (EPI == EPI_GATED_BWD)
@@ -572,10 +589,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
 }
 
 // ---------------------------------------------------------------- split kernel
-// (Rows of a tile past M or N: where one box holds the operand's 128 rows it is
-// cut to what exists, and the products of the rows below it, of whatever the
-// stage held, go to accumulators that nothing reads.)
-//
 // Products whose 128 x 128 tiles do not fill the GPU: a cluster of S CTAs
 // computes one tile, each a part of the contraction.  Each CTA finishes a
 // slice of the tile's columns: every CTA writes its FP32 accumulators to
@@ -583,7 +596,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1) gem
 // (shared memory to shared memory, complete on a barrier there), and adds what
 // it receives in rank order.  Nothing passes through HBM and one launch does
 // it.  (Loads from the other CTAs' shared memory instead were bound by their
-// latency: 22 us for 1024 x 4096 x 256 tokens with S = 8.)
+// latency: 22 us for 1024 x 4096 x 256 tokens with S = 8, 18 us now.)
+//
+// Where one box holds all 128 rows of an operand's tile, it is cut to the rows
+// that exist; the products of the rows below it, of whatever the stage held, go
+// to accumulators that nothing reads.
+//
+// What bounds it is its chain: 1800 cycles to set up, 1100 to the first block,
+// 610 a block, 500 to the accumulators, 1500 to stage them, 1700 for the slices,
+// 2300 for a piece (64 tokens through 1024 x 4096 in clusters of 8: 7.9 us).
 constexpr int SPLIT_STAGES = 5;
 constexpr int SPLIT_ACC = GEMM_BM * 128 * 4;   // a tile's accumulators
 constexpr int SPLIT_SMEM = SPLIT_STAGES * GEMM_STAGE + SPLIT_ACC + 1024;

@@ -182,8 +182,8 @@ constexpr Place ALONE = {false, false};
 // One launch: D[M, N] over contraction K of a[0] and b[0] (and of a[1], b[1]
 // where given: `groups` == 1 adds their product to the same D, 2 computes a
 // second D of a[1] and b[0]).  The epilogue fields of p are the caller's.
-qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt, const View* a0, const View* a1, const View* b0,
-                    const View* b1, int64_t M, int64_t N, int64_t K, int groups, Place place, cudaStream_t s)
+qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt, const View* a0, const View* a1,
+                    const View* b0, const View* b1, int64_t M, int64_t N, int64_t K, int groups, Place place, cudaStream_t s)
 {
     int sms = 0;
     if (query_device(&sms, &p.err) != cudaSuccess) return QTA_ERR_CUDA;
@@ -270,7 +270,10 @@ GemmParams blank()
 
 // Workspace of the backward products: 16-bit intermediates of `width`
 // channels with rows on 16 bytes, then the partial column sums.
-size_t mid_bytes(int64_t rows, int64_t width) { return static_cast<size_t>(round_up(rows * round_up(width, 8) * 2, 256)); }
+size_t mid_bytes(int64_t rows, int64_t width)
+{
+    return static_cast<size_t>(round_up(rows * round_up(width, 8) * 2, 256));
+}
 View mid_view(void* ws, int i, int64_t rows, int64_t width)
 {
     View v;
@@ -430,7 +433,8 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     p.bias = bias;
     p.bias_dt = d->bias_dtype;
     p.out_dt = d->out_dtype;
-    return run_gemm(FORM_NT, EPI_LINEAR, p, {&vy, nullptr, residual ? &vr : nullptr}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+    return run_gemm(FORM_NT, EPI_LINEAR, p, {&vy, nullptr, residual ? &vr : nullptr},
+                    d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
                     ALONE, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -488,7 +492,8 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
         p.bias_dt = d->bias_dtype;
         p.out_dt = d->dtype;
         p.colsum = dbias ? part : nullptr;
-        st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, {&dz, nullptr, &vdy}, d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
+        st = run_gemm(FORM_NT, EPI_LINEAR_BWD, p, {&dz, nullptr, &vdy},
+                      d->dtype, &vx, nullptr, &vw, nullptr, d->rows, d->n_out, d->n_in, 1,
                       ALONE, cs);
         if (st != QTA_OK) return st;
     }
@@ -502,14 +507,16 @@ qta_status qta_linear_bwd(const qta_linear_desc* d, const qta_mat* dy, const qta
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1,
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr},
+                      d->dtype, &dz, nullptr, &vw, nullptr, d->rows, d->n_in, d->n_out, 1,
                       {dbias != nullptr, dw != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     if (dw) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdw, nullptr, nullptr}, d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1,
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdw, nullptr, nullptr},
+                      d->dtype, &dz, nullptr, &vx, nullptr, d->n_out, d->n_in, d->rows, 1,
                       {dx || dbias, dx != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
@@ -538,7 +545,8 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     GemmParams p = blank();
     p.act = d->act;
     p.out_dt = d->dtype;
-    return run_gemm(FORM_NT, EPI_GATED, p, {&vh, nullptr, nullptr}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
+    return run_gemm(FORM_NT, EPI_GATED, p, {&vh, nullptr, nullptr},
+                    d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
                     ALONE, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -582,21 +590,24 @@ qta_status qta_gated_ffn_bwd(const qta_ffn_desc* d, const qta_mat* dh, const qta
         GemmParams p = blank();
         p.act = d->act;
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, {&mg, &mu, &vdh}, d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
+        st = run_gemm(FORM_NT, EPI_GATED_BWD, p, {&mg, &mu, &vdh},
+                      d->dtype, &vx, nullptr, &vg, &vu, d->rows, d->width, d->hidden, 1,
                       ALONE, cs);
         if (st != QTA_OK) return st;
     }
     if (dx) {
         GemmParams p = blank();
         p.out_dt = d->dtype;
-        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr}, d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1,
+        st = run_gemm(FORM_NN, EPI_LINEAR, p, {&vdx, nullptr, nullptr},
+                      d->dtype, &mg, &mu, &vg, &vu, d->rows, d->hidden, d->width, 1,
                       {false, dwg != nullptr}, cs);
         if (st != QTA_OK) return st;
     }
     if (dwg) {
         GemmParams p = blank();
         p.out_dt = d->grad_dtype;
-        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdg, &vdu, nullptr}, d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2,
+        st = run_gemm(FORM_TN, EPI_LINEAR, p, {&vdg, &vdu, nullptr},
+                      d->dtype, &mg, &mu, &vx, nullptr, d->width, d->hidden, d->rows, 2,
                       {dx != nullptr, dx != nullptr}, cs);
         if (st != QTA_OK) return st;
     }

@@ -4,12 +4,15 @@
 // on G rows at a time.  The rows to come wait in shared memory: every thread
 // copies its own vectors of the next STAGES - 1 rows there asynchronously and
 // reads them back itself, so this ring needs no barrier and no registers.
-// What bounds the kernels is HBM, closely followed by instruction issue (a
-// first form with scalar arithmetic and a test per vector took 1056
-// instructions for four vectors of a row and reached 4.3 TB/s): arithmetic is
-// on pairs of FP32 values, gamma and beta are widened once into shared memory,
-// each thread's own columns, and the loops have no tests but for vectors that
-// cross a row's end.
+// What bounds the kernels is HBM and, before it, each row's chain of reductions
+// with 16 warps on an SM: 8192 x 4096 bf16 with a residual 49 us (5.5 TB/s, 81 %
+// of a copy), 8192 x 8192 87 to 92 us; backward 8192 x 5120 RMS 60 us + 6 for
+// the column sums (5.0 TB/s together).  Issue is 40 % busy; a first form with
+// scalar arithmetic and a test per vector took 1056 instructions for four
+// vectors of a row and reached 4.3 TB/s.  So arithmetic is on pairs of FP32
+// values, gamma and beta are widened once into shared memory, each thread's own
+// columns, and the loops have no tests but for vectors that cross a row's end.
+// (640 or 768 threads on an SM instead of 512 were no faster.)
 //
 // Rows may start anywhere: where every matrix of a call has its rows at the
 // same distance from a 16-byte boundary (one base alignment, row distances
@@ -659,7 +662,8 @@ cudaError_t launch_norm_bwd_1(const NormBwdParams& p, const RowPlan& q, cudaStre
 {
     // (the ring holds the sums afterwards: 8 bytes for each element of a row's slots, half of it with two matrices)
     NormBwdParams pp = p;
-    const int ring = VPT * 16 * q.T * q.G * BWD_STAGES<VPT> * (RES ? 3 : 2), weights = VPT * 16 * q.T * (Vec<DT>::N / 4);
+    const int ring = VPT * 16 * q.T * q.G * BWD_STAGES<VPT> * (RES ? 3 : 2);
+    const int weights = VPT * 16 * q.T * (Vec<DT>::N / 4);
     pp.w_smem = ring + weights <= ROW_SMEM;
     const int smem = ring + (pp.w_smem ? weights : 0);
     static std::atomic<unsigned> done{0};

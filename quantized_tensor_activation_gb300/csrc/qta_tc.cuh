@@ -117,7 +117,10 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // The same in two steps, without ordering memory.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // Address of `p` (shared memory of this CTA) in the even CTA of the pair.
