@@ -352,98 +352,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     const int per_group = p.tiles_m * p.tiles_n;
     const int n_tiles = per_group * p.groups;
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, done = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int t = first; ok && t < n_tiles; t += step) {
-                const int g = t / per_group, r = t - g * per_group;
-                int tm, tn;
-                tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
-                const int m0 = (tm * 2 + rank) * GEMM_BM, n0 = tn * TILE_N;
-                const int nb = DUAL ? n0 : n0 + rank * (BN / 2);   // this CTA's rows of B
-                for (int kb = 0; kb < p.nk; ++kb) {
-                    if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const int second = kb >= p.nk0;
-                    const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
-                    const CUtensorMap* ma = &p.a[second | g];
-                    const CUtensorMap* mb = &p.b[second];
-                    uint8_t* sa = smem + s * GEMM_STAGE;
-                    uint8_t* sb = sa + GEMM_A_BYTES;
-                    auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
-                        tma_load_2d_pair(dst, map, c0, c1, leader_addr(&full[s]));
-                    };
+        const bool lead = elect_lane();
+        int s = 0, done = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += step) {
+            const int g = t / per_group, r = t - g * per_group;
+            int tm, tn;
+            tile_coords(r, p.tiles_m, p.tiles_n, tm, tn);
+            const int m0 = (tm * 2 + rank) * GEMM_BM, n0 = tn * TILE_N;
+            const int nb = DUAL ? n0 : n0 + rank * (BN / 2);   // this CTA's rows of B
+            for (int kb = 0; kb < p.nk; ++kb) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1u, p.err)) {
+                    ok = false;
+                    break;
+                }
+                const int second = kb >= p.nk0;
+                const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
+                const CUtensorMap* ma = &p.a[second | g];
+                const CUtensorMap* mb = &p.b[second];
+                uint8_t* sa = smem + s * GEMM_STAGE;
+                uint8_t* sb = sa + GEMM_A_BYTES;
+                const uint32_t bar = leader_addr(&full[s]);
+                if (lead) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * GEMM_STAGE);
                     if constexpr (A_MN) {
 #pragma unroll
-                        for (int i = 0; i < GEMM_BM / 64; ++i) load(sa + i * BOX_BYTES, ma, m0 + 64 * i, k0);
+                        for (int i = 0; i < GEMM_BM / 64; ++i)
+                            tma_load_2d_pair(sa + i * BOX_BYTES, ma, m0 + 64 * i, k0, bar);
                     } else {
-                        load(sa, ma, k0, m0);
+                        tma_load_2d_pair(sa, ma, k0, m0, bar);
                     }
                     if constexpr (DUAL) {
-                        load(sb, &p.b[rank], k0, nb);
+                        tma_load_2d_pair(sb, &p.b[rank], k0, nb, bar);
                     } else if constexpr (B_MN) {
 #pragma unroll
-                        for (int i = 0; i < BN / 2 / 64; ++i) load(sb + i * BOX_BYTES, mb, nb + 64 * i, k0);
+                        for (int i = 0; i < BN / 2 / 64; ++i)
+                            tma_load_2d_pair(sb + i * BOX_BYTES, mb, nb + 64 * i, k0, bar);
                     } else {
-                        load(sb, mb, k0, nb);
-                    }
-                    ++done;
-                    if (++s == GEMM_STAGES) {
-                        s = 0;
-                        ph ^= 1u;
+                        tma_load_2d_pair(sb, mb, k0, nb, bar);
                     }
                 }
-            }
-            // let the loads in flight land before the shared memory goes away (with a pair, the even CTA's barriers
-            // count both CTAs' loads, and neither leaves before both are here)
-            if (!ok && rank == 0) {
-                const int n = done < GEMM_STAGES ? done : GEMM_STAGES;
-                const uint64_t until = globaltimer_ns() + 2000000000ull;
-                for (int i = 1; i <= n; ++i) {
-                    const int j = done - i;
-                    mbar_wait_until(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1u, until);
+                ++done;
+                if (++s == GEMM_STAGES) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
+        // let the loads in flight land before the shared memory goes away (with a pair, the even CTA's barriers
+        // count both CTAs' loads, and neither leaves before both are here)
+        if (!ok && rank == 0) {
+            const int n = done < GEMM_STAGES ? done : GEMM_STAGES;
+            const uint64_t until = globaltimer_ns() + 2000000000ull;
+            for (int i = 1; i <= n; ++i) {
+                const int j = done - i;
+                mbar_wait_until(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1u, until);
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool lead = elect_lane();
             int s = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int t = first; ok && t < n_tiles; t += step, ++it) {
                 const int buf = it & 1;
                 const uint32_t drained = ((it >> 1) & 1) ^ 1u;
-                if (!mbar_wait_cluster(&acc_empty[buf], drained, p.err)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[buf], drained, p.err))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 for (int kb = 0; kb < p.nk; ++kb) {
-                    if (!mbar_wait(&full[s], ph, p.err)) {
+                    if (!mbar_wait_warp(&full[s], ph, p.err)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
                     const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
+                    if (lead) {
 #pragma unroll
-                    for (int k = 0; k < GEMM_BK / 16; ++k)
-                        tc_mma<2>(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
-                               kb > 0 || k > 0);
-                    tc_commit<2>(&empty[s]);
+                        for (int k = 0; k < GEMM_BK / 16; ++k)
+                            tc_mma<2>(tmem + buf * BN, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc,
+                                      kb > 0 || k > 0);
+                        tc_commit<2>(&empty[s]);
+                    }
                     if (++s == GEMM_STAGES) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (ok) tc_commit<2>(&acc_full[buf]);
+                if (ok && lead) tc_commit<2>(&acc_full[buf]);
             }
             if (!ok) {   // the products in flight end before TMEM is freed
-                tc_commit<2>(&drain);
+                if (lead) tc_commit<2>(&drain);
                 mbar_wait_until(&drain, 0, globaltimer_ns() + 2000000000ull);
             }
         }
@@ -738,21 +742,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
-            bool ok = true;
-            int done = 0;
-            for (int kb = kb0; kb < kb1; ++kb, ++done) {
-                const int s = done % SPLIT_STAGES;
-                if (done >= SPLIT_STAGES && !mbar_wait(&empty[s], (done / SPLIT_STAGES - 1) & 1, p.err)) {
-                    ok = false;
-                    break;
-                }
-                const int second = kb >= p.nk0;
-                const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
-                const CUtensorMap* ma = &p.a[second | g];
-                const CUtensorMap* mb = &p.b[second];
-                uint8_t* sa = smem + s * GEMM_STAGE;
-                uint8_t* sb = sa + GEMM_A_BYTES;
+        const bool lead = elect_lane();
+        bool ok = true;
+        int s = 0, done = 0;
+        uint32_t ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++done) {
+            if (!mbar_wait_warp(&empty[s], ph ^ 1u, p.err)) {
+                ok = false;
+                break;
+            }
+            const int second = kb >= p.nk0;
+            const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
+            const CUtensorMap* ma = &p.a[second | g];
+            const CUtensorMap* mb = &p.b[second];
+            uint8_t* sa = smem + s * GEMM_STAGE;
+            uint8_t* sb = sa + GEMM_A_BYTES;
+            if (lead) {
                 mbar_arrive_expect_tx(&full[s], p.stage_bytes);
                 if constexpr (A_MN) {
                     tma_load_2d(sa, ma, m0, k0, &full[s]);
@@ -762,43 +767,53 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
                 }
                 if constexpr (DUAL) {
                     tma_load_2d(sb, &p.b[0], k0, n0, &full[s]);
-                    tma_load_2d(sb + GEMM_A_BYTES / 2, &p.b[1], k0, n0, &full[s]);
+                    tma_load_2d(sb + TILE_N * GEMM_BK * 2, &p.b[1], k0, n0, &full[s]);
                 } else if constexpr (B_MN) {
-                    tma_load_2d(sb, mb, n0, k0, &full[s]);
-                    tma_load_2d(sb + BOX_BYTES, mb, n0 + 64, k0, &full[s]);
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i) tma_load_2d(sb + i * BOX_BYTES, mb, n0 + 64 * i, k0, &full[s]);
                 } else {
                     tma_load_2d(sb, mb, k0, n0, &full[s]);
                 }
             }
-            if (!ok) {   // let the loads in flight land before the shared memory goes away
-                failed = 1;
-                const uint64_t until = globaltimer_ns() + 2000000000ull;
-                for (int j = done > SPLIT_STAGES ? done - SPLIT_STAGES : 0; j < done; ++j)
-                    mbar_wait_until(&full[j % SPLIT_STAGES], (j / SPLIT_STAGES) & 1, until);
+            if (++s == SPLIT_STAGES) {
+                s = 0;
+                ph ^= 1u;
             }
         }
+        if (!ok) {   // let the loads in flight land before the shared memory goes away
+            failed = 1;
+            const uint64_t until = globaltimer_ns() + 2000000000ull;
+            for (int j = done > SPLIT_STAGES ? done - SPLIT_STAGES : 0; j < done; ++j)
+                mbar_wait_until(&full[j % SPLIT_STAGES], (j / SPLIT_STAGES) & 1, until);
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < kb1 - kb0; ++i) {
-                const int s = i % SPLIT_STAGES;
-                if (!mbar_wait(&full[s], (i / SPLIT_STAGES) & 1, p.err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
-                const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
+        const bool lead = elect_lane();
+        bool ok = true;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(&full[s], ph, p.err)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
+            const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
+            if (lead) {
 #pragma unroll
                 for (int k = 0; k < GEMM_BK / 16; ++k)
-                    tc_mma<1>(tmem, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc, i > 0 || k > 0);
+                    tc_mma<1>(tmem, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc, kb > kb0 || k > 0);
                 tc_commit<1>(&empty[s]);
             }
-            tc_commit<1>(&acc_full);
-            if (!ok) {   // the products in flight end before TMEM is freed
-                failed = 1;
-                mbar_wait_until(&acc_full, 0, globaltimer_ns() + 2000000000ull);
+            if (++s == SPLIT_STAGES) {
+                s = 0;
+                ph ^= 1u;
             }
+        }
+        if (lead) tc_commit<1>(&acc_full);
+        if (!ok) {   // the products in flight end before TMEM is freed
+            failed = 1;
+            mbar_wait_until(&acc_full, 0, globaltimer_ns() + 2000000000ull);
         }
     }
     __syncwarp();

@@ -86,6 +86,25 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
             : "memory");
 }
 
+// True in one lane of the warp, the same one at every call.  tcgen05 and TMA
+// instructions take their descriptors from uniform registers.  A warp that
+// stays together up to `if (lead)` around the instructions alone has them
+// there; inside a loop that only lane 0 runs each instruction first collects
+// its operands, and a block's four products took 206 cycles to issue (20 so).
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+    return lead != 0;
+}
+
+// mbar_wait by a whole warp, with one answer for all of it.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned int* err)
+{
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, err));
+}
+
 // The mbarrier (with a pair: the one at this offset in both CTAs) completes
 // when every tcgen05.mma this thread has issued is done.
 template <int CG>
