@@ -1,4 +1,6 @@
 // qta_gemm.cu -- instantiations and launcher of the matrix-product kernels.
+#include <climits>
+#include <cstdint>
 #include "qta_layer.cuh"
 
 namespace qta {
@@ -11,13 +13,13 @@ static int resident_clusters(int size, int sms)
     const int i = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
     int n = cache[i].load();
     if (n) return n;
-    auto fn = gemm_split_kernel<false, false, EPI_LINEAR>;
+    auto fn = gemm_split_kernel<128, false, false, EPI_LINEAR>;
     static std::atomic<unsigned> done{0};
-    if (ensure_smem_attr(reinterpret_cast<const void*>(fn), SPLIT_SMEM, &done) != cudaSuccess) return 0;
+    if (ensure_smem_attr(reinterpret_cast<const void*>(fn), SplitCfg<128>::SMEM, &done) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms / size * size));
     cfg.blockDim = dim3(GEMM_THREADS);
-    cfg.dynamicSmemBytes = SPLIT_SMEM;
+    cfg.dynamicSmemBytes = SplitCfg<128>::SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
@@ -30,24 +32,45 @@ static int resident_clusters(int size, int sms)
 }
 
 // Pairs of CTAs on 256 x 256 tiles where the 128 x 128 tiles are more than the
-// SMs, else the split kernel on those (1021 x 1000 -> 1096, bf16: 9 us against
-// 22 in 20 pairs).  The contraction of each is split while the clusters are
-// resident at once (in half the GPU where two such launches run side by side)
-// and a CTA keeps at least 4 blocks: a block takes 0.30 us, the join as long
-// as 5 to 8 of them (512 x 1024, S = 1, 2, 4: 16 blocks 9.8, 8.2, 8.1 us; 8
-// blocks 7.1, 6.5, 7.2 us; 1021 x 1096: 16 blocks 9.9, 8.9 us; 8 blocks 7.2,
-// 7.4 us).
-constexpr int SPLIT_MIN_BLOCKS = 12;
-
+// SMs, else the split kernel (1021 x 1000 -> 1096, bf16: 9 us against 22 in 20
+// pairs), whose tile and split are those of the least estimated time among the
+// ones whose clusters are all resident at once (in half the GPU where two such
+// launches run side by side).  The estimate, in ns: a block of 64 of the
+// contraction takes 220 on 128 columns and 195 on 64 (both bound by issue and
+// latency, not by bytes), 128 columns 400 more to write out, the join of a
+// split contraction 2400 and 1300.  Measured, 128 columns split in 1, 2, 4, 8
+// and 64 columns split in 1, 2, 4, us:
+//     64 x 512, K 4096:   17.7 12.1  8.5  6.9    14.9 10.0  7.3
+//     33 x 1024, K 1024:   6.0  6.0  4.9  5.0     5.4  5.0  4.3
+//     128 x 1024, K 512:   5.1  6.1  6.0  7.1     4.3  4.7  4.5
+//     512 x 1024, K 4096: 17.6 12.7 10.7  -      15.5 11.4  -
+//     256 x 4096, K 2048: 10.9 10.2   -   -       9.7   -   -
+//     64 x 8192, K 4096:  18.9 16.0   -   -      16.0   -   -
+// Over 100 such shapes the choice takes 0.8 % longer than the best on average.
 GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared)
 {
     const bool dual = epi == EPI_GATED || epi == EPI_GATED_BWD;
-    const int64_t tile_n = dual ? 64 : 128, tiles = ((M + 127) / 128) * ((N + tile_n - 1) / tile_n) * groups;
-    if (tiles > sms) return {256, dual ? 128 : 256, 128, 0};
-    int s = 1;
-    if (blocks >= SPLIT_MIN_BLOCKS)
-        while (s < 8 && tiles * (shared ? 2 : 1) <= resident_clusters(2 * s, sms) && blocks >= 4 * (2 * s)) s *= 2;
-    return {128, static_cast<int>(tile_n), static_cast<int>(tile_n), s};
+    const auto tiles = [&](int bn) {
+        const int64_t cols = dual ? bn / 2 : bn;
+        return (M + 127) / 128 * ((N + cols - 1) / cols) * groups;
+    };
+    if (tiles(128) > sms) return {256, dual ? 128 : 256, 128, 0, 256};
+    GemmTile best = {};
+    int64_t least = INT64_MAX;
+    for (const int bn : {128, 64}) {
+        const int cols = dual ? bn / 2 : bn;
+        for (int s = 1; s <= bn / 16 && s <= blocks; s *= 2) {
+            const bool fallback = bn == 128 && s == 1;
+            if (!fallback && tiles(bn) * (shared ? 2 : 1) > resident_clusters(s, sms)) break;
+            const int64_t ns = (blocks + s - 1) / s * (bn == 128 ? 220 : 195) + (bn == 128 ? 400 : 0) +
+                               (s == 1 ? 0 : bn == 128 ? 2400 : 1300);
+            if (ns < least) {
+                least = ns;
+                best = {128, cols, cols, s, bn};
+            }
+        }
+    }
+    return best;
 }
 
 template <bool A_MN, bool B_MN, int EPI>
@@ -75,19 +98,19 @@ static cudaError_t launch_pairs(const GemmParams& p, int sms, cudaStream_t strea
                       stream, q);
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <int BN, bool A_MN, bool B_MN, int EPI>
 static cudaError_t launch_split(const GemmParams& p, cudaStream_t stream)
 {
     static std::atomic<unsigned> done{0};
-    auto fn = gemm_split_kernel<A_MN, B_MN, EPI>;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), SPLIT_SMEM, &done);
+    auto fn = gemm_split_kernel<BN, A_MN, B_MN, EPI>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), SplitCfg<BN>::SMEM, &done);
     if (e != cudaSuccess) return e;
     GemmParams q = p;
-    q.idesc |= idesc_f16(GEMM_BM, 128, false, A_MN, B_MN);
+    q.idesc |= idesc_f16(GEMM_BM, BN, false, A_MN, B_MN);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_m * p.tiles_n * p.groups * p.split));
     cfg.blockDim = dim3(GEMM_THREADS);
-    cfg.dynamicSmemBytes = SPLIT_SMEM;
+    cfg.dynamicSmemBytes = SplitCfg<BN>::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -103,7 +126,9 @@ static cudaError_t launch_split(const GemmParams& p, cudaStream_t stream)
 template <bool A_MN, bool B_MN, int EPI>
 static cudaError_t launch_t(const GemmParams& p, int sms, cudaStream_t stream)
 {
-    return p.split ? launch_split<A_MN, B_MN, EPI>(p, stream) : launch_pairs<A_MN, B_MN, EPI>(p, sms, stream);
+    if (p.bn == 256) return launch_pairs<A_MN, B_MN, EPI>(p, sms, stream);
+    if (p.bn == 128) return launch_split<128, A_MN, B_MN, EPI>(p, stream);
+    return launch_split<64, A_MN, B_MN, EPI>(p, stream);
 }
 
 cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream)

@@ -66,6 +66,7 @@ struct GemmParams {
     // boxes of 32 rows x epi_box_cols; else by per-thread loads and stores
     int staged;
     CUtensorMap aux_map, out_map[2];
+    int bn;                     // accumulator columns of a tile: 256 (pairs), 128 or 64 (split kernel)
     int split;                  // CTAs that share a tile's contraction (split kernel)
     int stage_bytes;            // what TMA writes of a stage (split kernel: boxes hold no rows past M and N)
     // The launch reads nothing that the launch before it on the stream writes,
@@ -84,7 +85,7 @@ constexpr int GEMM_THREADS = 64 + 32 * GEMM_EPI_WARPS;
 constexpr int EPI_BUF = 4096;   // a staging buffer of an epilogue warp: 32 rows x 128 bytes; each warp has two
 
 // A stage holds 128 rows of A and 128 of B: the pair's tile is 256 x 256, each
-// CTA with its half of both; the split kernel's 128 x 128.
+// CTA with its half of both; the split kernel's 128 x 128 or 128 x 64.
 constexpr int GEMM_A_BYTES = GEMM_BM * GEMM_BK * 2;
 constexpr int GEMM_STAGE = 2 * GEMM_A_BYTES;
 constexpr int GEMM_SMEM =   // with slack to start on 1024 bytes
@@ -594,7 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 
 // ---------------------------------------------------------------- split kernel
 // Products whose 128 x 128 tiles do not fill the GPU: a cluster of S CTAs
-// computes one tile, each a part of the contraction.  Each CTA finishes a
+// computes one tile of BN = 128 or 64 accumulator columns, each a part of the
+// contraction.  Each CTA finishes a
 // slice of the tile's columns: every CTA writes its FP32 accumulators to
 // shared memory slice by slice, sends each slice to its CTA in one bulk copy
 // (shared memory to shared memory, complete on a barrier there), and adds what
@@ -609,9 +611,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 // What bounds it is its chain: 1800 cycles to set up, 1100 to the first block,
 // 610 a block, 500 to the accumulators, 1500 to stage them, 1700 for the slices,
 // 2300 for a piece (64 tokens through 1024 x 4096 in clusters of 8: 7.9 us).
-constexpr int SPLIT_STAGES = 5;
-constexpr int SPLIT_ACC = GEMM_BM * 128 * 4;   // a tile's accumulators
-constexpr int SPLIT_SMEM = SPLIT_STAGES * GEMM_STAGE + SPLIT_ACC + 1024;
+template <int BN>
+struct SplitCfg {
+    static constexpr int STAGE = GEMM_A_BYTES + BN * GEMM_BK * 2;
+    static constexpr int STAGES = BN == 128 ? 5 : 7;
+    static constexpr int ACC = GEMM_BM * BN * 4;   // a tile's accumulators
+    static constexpr int SMEM = STAGES * STAGE + ACC + 1024;
+};
 
 // Byte of 16-byte piece `k` of row `row` in a slice with rows of `bytes` (64 or
 // more): pieces are permuted so that 8 rows' accesses to one piece cover all banks.
@@ -657,13 +663,13 @@ __device__ __forceinline__ void split_piece(const GemmParams& p, int g, int row0
 
 // The pieces of this CTA's slice: `own` is its own part, `received` +
 // k * slice_bytes that of CTA k.
-template <int EPI, int W>
+template <int EPI, int BN, int W>
 __device__ __forceinline__ void split_pieces(const GemmParams& p, const uint8_t* own, const uint8_t* received, int rank,
                                              int g, int m0, int n0, int warp, int lane)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
-    const int S = p.split, row_bytes = 128 * 4 / S, slice_bytes = GEMM_BM * row_bytes;
-    const int cols = (DUAL ? 64 : 128) / S;   // output columns of the slice
+    const int S = p.split, row_bytes = BN * 4 / S, slice_bytes = GEMM_BM * row_bytes;
+    const int cols = (DUAL ? BN / 2 : BN) / S;   // output columns of the slice
 #pragma unroll 1
     for (int u0 = warp; u0 < 4 * (cols / W); u0 += GEMM_EPI_WARPS) {
         const int q = u0 & 3, c = (u0 >> 2) * W, col = n0 + rank * cols + c, row0 = m0 + 32 * q;
@@ -689,13 +695,14 @@ __device__ __forceinline__ void split_pieces(const GemmParams& p, const uint8_t*
     }
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <int BN, bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __grid_constant__ GemmParams p)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
-    constexpr int BN = 128, TILE_N = DUAL ? BN / 2 : BN;
+    using C = SplitCfg<BN>;
+    constexpr int TILE_N = DUAL ? BN / 2 : BN, TILE_LOG = (BN == 128 ? 7 : 6) - (DUAL ? 1 : 0);
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[SPLIT_STAGES], empty[SPLIT_STAGES], acc_full, recv_full;
+    __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full, recv_full;
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
 
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     }
     const int live = min(GEMM_BM, p.M - m0);   // rows of the tile in range
     if (warp == 0) {
-        if (lane < SPLIT_STAGES) {
+        if (lane < C::STAGES) {
             mbar_init(&full[lane], 1);
             mbar_init(&empty[lane], 1);
         } else if (lane == 30) {
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             const int k0 = (second ? kb - p.nk0 : kb) * GEMM_BK;
             const CUtensorMap* ma = &p.a[second | g];
             const CUtensorMap* mb = &p.b[second];
-            uint8_t* sa = smem + s * GEMM_STAGE;
+            uint8_t* sa = smem + s * C::STAGE;
             uint8_t* sb = sa + GEMM_A_BYTES;
             if (lead) {
                 mbar_arrive_expect_tx(&full[s], p.stage_bytes);
@@ -775,7 +782,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
                     tma_load_2d(sb, mb, k0, n0, &full[s]);
                 }
             }
-            if (++s == SPLIT_STAGES) {
+            if (++s == C::STAGES) {
                 s = 0;
                 ph ^= 1u;
             }
@@ -783,8 +790,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
         if (!ok) {   // let the loads in flight land before the shared memory goes away
             failed = 1;
             const uint64_t until = globaltimer_ns() + 2000000000ull;
-            for (int j = done > SPLIT_STAGES ? done - SPLIT_STAGES : 0; j < done; ++j)
-                mbar_wait_until(&full[j % SPLIT_STAGES], (j / SPLIT_STAGES) & 1, until);
+            for (int j = done > C::STAGES ? done - C::STAGES : 0; j < done; ++j)
+                mbar_wait_until(&full[j % C::STAGES], (j / C::STAGES) & 1, until);
         }
     } else if (warp == 1) {
         const bool lead = elect_lane();
@@ -797,15 +804,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
                 break;
             }
             tc_fence_after();
-            const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * GEMM_STAGE));
-            const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * GEMM_STAGE + GEMM_A_BYTES));
+            const uint64_t da = smem_desc<A_MN>(smem_u32(smem + s * C::STAGE));
+            const uint64_t db = smem_desc<B_MN>(smem_u32(smem + s * C::STAGE + GEMM_A_BYTES));
             if (lead) {
 #pragma unroll
                 for (int k = 0; k < GEMM_BK / 16; ++k)
                     tc_mma<1>(tmem, da + k * K16_STEP<A_MN>, db + k * K16_STEP<B_MN>, p.idesc, kb > kb0 || k > 0);
                 tc_commit<1>(&empty[s]);
             }
-            if (++s == SPLIT_STAGES) {
+            if (++s == C::STAGES) {
                 s = 0;
                 ph ^= 1u;
             }
@@ -825,7 +832,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
         const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
         if (S == 1) {   // the whole sum is here
 #pragma unroll 1
-            for (int c = half * (TILE_N / 2); c < (half + 1) * (TILE_N / 2) && !failed; c += 32) {
+            for (int c = 32 * half; c < TILE_N && !failed; c += 64) {
                 float v[32], u[DUAL ? 32 : 1];
                 tmem_ld32(acc + c, v);
                 if constexpr (DUAL) {
@@ -852,7 +859,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             // accumulators to shared memory by slices, over the operand ring (every product has read it by now)
             const int row_bytes = BN * 4 / S, slice_bytes = GEMM_BM * row_bytes;
             const int ls = S == 2 ? 1 : S == 4 ? 2 : 3;
-            uint8_t* received = smem + SPLIT_STAGES * GEMM_STAGE;
+            uint8_t* received = smem + C::STAGES * C::STAGE;
 #pragma unroll 1
             for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
                 float v[32];
@@ -862,7 +869,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
                 for (int i = 0; i < 8; ++i) {
                     // the gated forms' slice: its columns of G, then the same of U
                     const int j = (c0 + 4 * i) & (TILE_N - 1), width = TILE_N >> ls;
-                    const int slice = j >> ((DUAL ? 6 : 7) - ls), at = (j & (width - 1)) + (c0 >= TILE_N ? width : 0);
+                    const int slice = j >> (TILE_LOG - ls), at = (j & (width - 1)) + (c0 >= TILE_N ? width : 0);
                     *reinterpret_cast<float4*>(smem + slice * slice_bytes + slice_at(32 * q + lane, at / 4, row_bytes)) =
                         make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
@@ -879,9 +886,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
             if (!failed) {
                 const uint8_t* own = smem + rank * slice_bytes;
                 if (TILE_N / S >= 16)
-                    split_pieces<EPI, 16>(p, own, received, rank, g, m0, n0, warp - 2, lane);
+                    split_pieces<EPI, BN, 16>(p, own, received, rank, g, m0, n0, warp - 2, lane);
                 else
-                    split_pieces<EPI, 8>(p, own, received, rank, g, m0, n0, warp - 2, lane);
+                    split_pieces<EPI, BN, 8>(p, own, received, rank, g, m0, n0, warp - 2, lane);
             }
         }
     } else if (S > 1) {

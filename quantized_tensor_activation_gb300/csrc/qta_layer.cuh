@@ -22,9 +22,10 @@ cudaError_t launch_col_finish(const float* part, int64_t stride, int parts, int6
 enum GemmForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
 
 // Tile of a product: output rows and columns, rows of the TMA box of a
-// contraction-contiguous B, CTAs that split its contraction (0: a pair's tile).
+// contraction-contiguous B, CTAs that split its contraction (0: a pair's tile),
+// accumulator columns.
 struct GemmTile {
-    int rows, cols, b_box, split;
+    int rows, cols, b_box, split, bn;
 };
 GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared);
 cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);

@@ -193,9 +193,10 @@ qta_status run_gemm(int form, int epi, GemmParams& p, const Outs& o, int32_t dt,
     const GemmTile t = gemm_tile(epi, M, N, p.nk, groups, sms, place.shared);
     p.beside = place.beside;
     p.split = t.split;
+    p.bn = t.bn;
     int a_rows = form == FORM_TN ? 64 : GEMM_BM, b_rows = form == FORM_NT ? t.b_box : 64;
     if (t.split) {   // no more rows than there are, in groups of 8 (the swizzle's)
-        const int a_boxes = form == FORM_TN ? 2 : 1, b_boxes = form == FORM_NT ? (dual ? 2 : 1) : 2;
+        const int a_boxes = form == FORM_TN ? 2 : 1, b_boxes = form == FORM_NT ? (dual ? 2 : 1) : t.bn / 64;
         if (form != FORM_TN && M < a_rows) a_rows = static_cast<int>(round_up(M, 8));
         if (form == FORM_NT && N < b_rows) b_rows = static_cast<int>(round_up(N, 8));
         p.stage_bytes = (a_rows * a_boxes + b_rows * b_boxes) * GEMM_BK * 2;
