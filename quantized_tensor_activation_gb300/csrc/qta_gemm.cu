@@ -1,4 +1,5 @@
 // qta_gemm.cu -- instantiations and launcher of the matrix-product kernels.
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 #include "qta_layer.cuh"
@@ -98,29 +99,60 @@ static cudaError_t launch_pairs(const GemmParams& p, int sms, cudaStream_t strea
                       stream, q);
 }
 
-template <int BN, bool A_MN, bool B_MN, int EPI>
-static cudaError_t launch_split(const GemmParams& p, cudaStream_t stream)
+// A launch of the split kernel's CTAs in clusters of `split`.
+template <typename... Params>
+static cudaError_t launch_clusters(void (*fn)(Params...), int ctas, int split, int smem, std::atomic<unsigned>* done,
+                                   cudaStream_t stream, Params... params)
 {
-    static std::atomic<unsigned> done{0};
-    auto fn = gemm_split_kernel<BN, A_MN, B_MN, EPI>;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), SplitCfg<BN>::SMEM, &done);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(fn), smem, done);
     if (e != cudaSuccess) return e;
-    GemmParams q = p;
-    q.idesc |= idesc_f16(GEMM_BM, BN, false, A_MN, B_MN);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_m * p.tiles_n * p.groups * p.split));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(GEMM_THREADS);
-    cfg.dynamicSmemBytes = SplitCfg<BN>::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.x = split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fn, q);
+    return cudaLaunchKernelEx(&cfg, fn, params...);
+}
+
+static int split_ctas(const GemmParams& p) { return p.tiles_m * p.tiles_n * p.groups * p.split; }
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+static cudaError_t launch_split(const GemmParams& p, cudaStream_t stream)
+{
+    static std::atomic<unsigned> done{0};
+    GemmParams q = p;
+    q.idesc |= idesc_f16(GEMM_BM, BN, false, A_MN, B_MN);
+    return launch_clusters(gemm_split_kernel<BN, A_MN, B_MN, EPI>, split_ctas(p), p.split, SplitCfg<BN>::SMEM, &done,
+                           stream, q);
+}
+
+template <int BN_X, int BN_W>
+static cudaError_t launch_both(const GemmParams& x, const GemmParams& w, cudaStream_t stream)
+{
+    static std::atomic<unsigned> done{0};
+    GemmParams qx = x, qw = w;
+    qx.idesc |= idesc_f16(GEMM_BM, BN_X, false, false, true);
+    qw.idesc |= idesc_f16(GEMM_BM, BN_W, false, true, true);
+    return launch_clusters(gemm_split_both_kernel<BN_X, BN_W>, split_ctas(x) + split_ctas(w), x.split,
+                           std::max(SplitCfg<BN_X>::SMEM, SplitCfg<BN_W>::SMEM), &done, stream, qx, qw, split_ctas(x));
+}
+
+bool launch_gemm_both(const GemmParams& x, const GemmParams& w, cudaStream_t stream, cudaError_t* e)
+{
+    if (!x.split || x.split != w.split) return false;
+    if (x.bn == 128)
+        *e = w.bn == 128 ? launch_both<128, 128>(x, w, stream) : launch_both<128, 64>(x, w, stream);
+    else
+        *e = w.bn == 128 ? launch_both<64, 128>(x, w, stream) : launch_both<64, 64>(x, w, stream);
+    return true;
 }
 
 template <bool A_MN, bool B_MN, int EPI>

@@ -696,7 +696,7 @@ __device__ __forceinline__ void split_pieces(const GemmParams& p, const uint8_t*
 }
 
 template <int BN, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __grid_constant__ GemmParams p)
+__device__ __forceinline__ void gemm_split(const GemmParams& p, int block)
 {
     constexpr bool DUAL = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
     using C = SplitCfg<BN>;
@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = p.split, rank = blockIdx.x % S;   // (the cluster's ranks are consecutive blocks)
-    const int t = blockIdx.x / S;
+    const int S = p.split, rank = block % S;   // (the cluster's ranks are consecutive blocks)
+    const int t = block / S;
     const int per_group = p.tiles_m * p.tiles_n;
     const int g = t / per_group, r = t - g * per_group;
     int tm, tn;
@@ -900,6 +900,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __gri
     tc_fence_after();
     if (warp == 1) tmem_dealloc<1>(tmem, BN);
     if (p.beside) pdl_wait();
+}
+
+template <int BN, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_split_kernel(const __grid_constant__ GemmParams p)
+{
+    gemm_split<BN, A_MN, B_MN, EPI>(p, blockIdx.x);
+}
+
+// The two products of a backward call in one launch: dx by the first `blocks_x`
+// CTAs, dw by the others.
+template <int BN_X, int BN_W>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    gemm_split_both_kernel(const __grid_constant__ GemmParams x, const __grid_constant__ GemmParams w, const int blocks_x)
+{
+    if (static_cast<int>(blockIdx.x) < blocks_x)
+        gemm_split<BN_X, false, true, EPI_LINEAR>(x, blockIdx.x);
+    else
+        gemm_split<BN_W, true, true, EPI_LINEAR>(w, blockIdx.x - blocks_x);
 }
 
 }  // namespace qta

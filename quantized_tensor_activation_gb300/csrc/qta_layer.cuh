@@ -30,6 +30,10 @@ struct GemmTile {
 GemmTile gemm_tile(int epi, int64_t M, int64_t N, int64_t blocks, int groups, int sms, bool shared);
 cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStream_t stream);
 
+// dx (FORM_NN) and dw (FORM_TN) in one launch, where both are the split
+// kernel's in clusters of one size; else nothing is launched.
+bool launch_gemm_both(const GemmParams& dx, const GemmParams& dw, cudaStream_t stream, cudaError_t* e);
+
 // Whether qta_skinny.cu takes a forward product: up to 16 tokens, and up to 32
 // where the contraction is short (n_in, tokens: its time against the split
 // kernel's; 1024, 32: 7.2 and 8.4 us; 2048, 32: 6.9 and 8.2; 3584, 32: 18.8 and
