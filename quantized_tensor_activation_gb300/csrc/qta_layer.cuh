@@ -34,11 +34,19 @@ cudaError_t launch_gemm(int form, int epi, const GemmParams& p, int sms, cudaStr
 // kernel's in clusters of one size; else nothing is launched.
 bool launch_gemm_both(const GemmParams& dx, const GemmParams& dw, cudaStream_t stream, cudaError_t* e);
 
-// Whether qta_skinny.cu takes a forward product: up to 16 tokens, and up to 32
-// where the contraction is short (n_in, tokens: its time against the split
-// kernel's; 1024, 32: 7.2 and 8.4 us; 2048, 32: 6.9 and 8.2; 3584, 32: 18.8 and
-// 15.2; 4096, 17: 9.1 and 7.4).
-inline bool skinny(int64_t rows, int64_t n_in) { return rows <= 16 || (rows <= 32 && n_in <= 2048); }
+// Whether qta_skinny.cu takes a forward product (`dual`: of two weights): up to
+// 8 tokens; up to 16 but for long contractions of two weights; up to 32 where the
+// contraction is short.  Its time against the split kernel's, us, n_in x outputs:
+//     one weight   16 tokens: 8192 x 2048 11.0, 11.1; 3584 x 8192 14.2, 14.0; 1024 x 1024 2.7, 4.2
+//                  32 tokens: 2048 x 4096  7.2,  7.8; 1024 x 1024  3.8,  4.3; 4096 x 1024 9.7, 7.2
+//     two          16 tokens: 2048 x 2048  6.8,  8.0; 3584 x 4096 12.6, 13.9; 4096 x  512 10.3, 7.2
+//                  32 tokens:  512 x 1024  3.6,  4.2; 1024 x  512  4.8,  4.6; 2048 x 2048 8.5, 8.0
+inline bool skinny(int64_t rows, int64_t n_in, bool dual)
+{
+    if (rows <= 8) return true;
+    if (rows <= 16) return !dual || n_in < 4096;
+    return rows <= 32 && n_in <= (dual ? 1024 : 2048);
+}
 
 struct SkinnyParams {
     const uint8_t* x;

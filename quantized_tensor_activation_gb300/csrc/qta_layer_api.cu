@@ -471,7 +471,7 @@ qta_status qta_linear(const qta_linear_desc* d, const qta_mat* x, const qta_mat*
     o.output(vy);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
-    if (skinny(d->rows, d->n_in))
+    if (skinny(d->rows, d->n_in, false))
         return run_skinny(d->dtype, vx, vw, nullptr, bias, d->bias_dtype, residual ? &vr : nullptr, vy, d->out_dtype,
                           d->act, reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();
@@ -571,7 +571,7 @@ qta_status qta_gated_ffn(const qta_ffn_desc* d, const qta_mat* x, const qta_mat*
     o.output(vh);
     if (o.any()) return QTA_ERR_INVALID_ARG;
 
-    if (skinny(d->rows, d->hidden))
+    if (skinny(d->rows, d->hidden, true))
         return run_skinny(d->dtype, vx, vg, &vu, nullptr, 0, nullptr, vh, d->dtype, d->act,
                           reinterpret_cast<cudaStream_t>(stream));
     GemmParams p = blank();
