@@ -7,21 +7,21 @@
 // contraction elements by TMA into a ring of shared-memory stages, warp 1
 // issues tcgen05.mma on them, warps 2-9 read the accumulators of the previous
 // tile (TMEM holds two) and run the epilogue.  In a pair each CTA loads and
-// keeps half of B, so a byte of shared memory feeds twice the products that it
-// feeds in a single CTA, whose 128 x 128 tile is bound by shared memory (8192 x
-// 8192 -> 3584 gated, fp16: 1004 us in single CTAs, 629 in pairs).  Products
-// too small for the pairs run the split kernel below.
+// keeps half of B, so a byte loaded feeds twice the products that it feeds in
+// a single CTA, whose 128 x 128 tiles are bound by what L2 gives (11.5 TB/s
+// over all SMs: 144 CTAs take 0.4 us a block, a pair 0.26 us for four times the
+// products).  Products too small for the pairs run the split kernel below.
 //
 // Operands whose contraction index is not the contiguous one (the backward
 // products) are read as they lie, with MN-major descriptors: nothing is
 // transposed in memory, and all three forms run at one rate.
 //
-// What bounds the pairs is the tensor cores: a block of a tile takes 605 cycles
-// with and without its loads (2170 TFLOP/s at 2.06 GHz).  Large products run at
-// the power limit (1.5 to 1.9 GHz): 8192^3 bf16 602 us, 1827 TFLOP/s, in bursts
-// of 20; 8192 x 8192 x 7168 fp16 1525 TFLOP/s for seconds on end.  The rest is
+// What bounds the pairs is the tensor cores: a block of a tile takes 528 to 540
+// cycles, waits included, of the 512 of its products.  Large products run at
+// the power limit (1.5 to 1.8 GHz): 8192^3 bf16 561 us, 1960 TFLOP/s, in bursts
+// of 20; 8192 x 8192 x 7168 fp16 1589 TFLOP/s for seconds on end.  The rest is
 // the last, partial round of tiles, the first loads (4000 cycles when they
-// come from HBM) and the last epilogue (5000 to 9000 cycles).
+// come from HBM) and the last epilogue (5000 to 10000 cycles).
 //
 // Accumulation on the tensor cores is FP32 that truncates: a sum over K terms
 // comes out small by about K 1e-9 of itself (K = 4096: 4e-6; rounded FP32 sums
@@ -608,9 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 // that exist; the products of the rows below it, of whatever the stage held, go
 // to accumulators that nothing reads.
 //
-// What bounds it is its chain: 1800 cycles to set up, 1100 to the first block,
-// 610 a block, 500 to the accumulators, 1500 to stage them, 1700 for the slices,
-// 2300 for a piece (64 tokens through 1024 x 4096 in clusters of 8: 7.9 us).
+// What bounds it is its chain, 3.2 us for 4 blocks and no join, and the blocks:
+// about 390 cycles each of issue and waits for 256 (BN = 64: 212) of products,
+// and L2's bandwidth where most SMs take part (64 tokens, 4096 -> 1024: 6.6 us;
+// 1021 x 1000 -> 1096: 7.9 us).
 template <int BN>
 struct SplitCfg {
     static constexpr int STAGE = GEMM_A_BYTES + BN * GEMM_BK * 2;
