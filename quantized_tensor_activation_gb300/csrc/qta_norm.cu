@@ -157,8 +157,8 @@ cudaError_t launch_norm_bwd_rows_fp32(const NormBwdParams&, const RowPlan&, cuda
 
 // Whether the row kernels take matrices whose rows start at these addresses
 // (n of them, NULL: absent), and the vectors of a row.
-static bool row_form(const void* const* base, const int64_t* ld, int n, int64_t cols, int dt, int max_threads,
-                     int* shift, int* aligned, RowPlan* q)
+static bool row_form(const void* const* base, const int64_t* ld, int n, int64_t rows, int64_t cols, int dt,
+                     int sms, int max_threads, int short_T, int* shift, int* aligned, RowPlan* q)
 {
     const int es = dt_size(dt), N = 16 / es;
     bool all = true;
@@ -171,7 +171,7 @@ static bool row_form(const void* const* base, const int64_t* ld, int n, int64_t 
     }
     *aligned = all && *shift == 0 && cols % N == 0;
     if (cols > (1 << 20)) return false;
-    return row_plan(*aligned ? cols / N : (cols + N - 1) / N + 1, max_threads, q);
+    return row_plan(*aligned ? cols / N : (cols + N - 1) / N + 1, rows, sms, max_threads, short_T, q);
 }
 
 static bool vec16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -183,7 +183,7 @@ cudaError_t launch_norm(const NormParams& in, int sms, cudaStream_t stream)
     const void* base[4] = {p.x, p.residual, p.y, p.sum};
     const int64_t ld[4] = {p.ld_x, p.ld_r, p.ld_y, p.ld_s};
     RowPlan q;
-    if (row_form(base, ld, 4, p.cols, p.dt, p.rows > sms ? FWD_MAX_THREADS : 32, &p.shift, &p.aligned, &q)) {
+    if (row_form(base, ld, 4, p.rows, p.cols, p.dt, sms, FWD_MAX_THREADS, 512, &p.shift, &p.aligned, &q)) {
         if (p.dt == 0) return launch_norm_rows_bf16(p, q, sms, stream);
         if (p.dt == 1) return launch_norm_rows_fp16(p, q, sms, stream);
         return launch_norm_rows_fp32(p, q, sms, stream);
@@ -202,7 +202,7 @@ cudaError_t launch_norm_bwd(const NormBwdParams& in, int sms, cudaStream_t strea
     RowPlan q;
     cudaError_t e;
     const unsigned nf = static_cast<unsigned>((p.cols + 31) / 32);
-    if (row_form(base, ld, 4, p.cols, p.dt, p.rows > sms ? BWD_MAX_THREADS : 32, &p.shift, &p.aligned, &q)) {
+    if (row_form(base, ld, 4, p.rows, p.cols, p.dt, sms, BWD_MAX_THREADS, 384, &p.shift, &p.aligned, &q)) {
         // CTAs: what fits on the GPU, or the rows; a multiple of 8 where the rows' shifts differ
         int64_t parts = (p.rows + q.G - 1) / q.G;
         if (parts > sms) parts = sms;

@@ -621,18 +621,33 @@ struct RowPlan {
     int vpt, T, G;
 };
 
-// Four vectors a thread wherever a row has them: a row's reductions and its
-// barrier cost each thread the same for two (RMS backward, 8192 x 5120 bf16:
-// 77 us with two).
-inline bool row_plan(int64_t nv, int max_threads, RowPlan* q)
+// Two vectors a thread where every row then has its threads at once (rows <= SMs
+// x rows of a CTA, `short_T` threads a row at most): the less code a thread runs,
+// the sooner a row that runs it once is done.  Four, two, us: forward 3 x 1808
+// fp16 6.7, 4.1; 1 x 8192 fp16 4.4, 3.3; 423 x 1116 fp32 5.5, 4.1; backward
+// 9 x 656 fp32 5.1, 3.9; 75 x 2440 fp32 6.1, 5.2; 1 x 8192 fp16 (512 threads)
+// 9.3, 10.2.  Else four wherever a row has them: a row's reductions and its
+// barrier cost each thread the same for two (RMS backward, 8192 x 5120 bf16: 77
+// us with two).
+inline bool row_plan(int64_t nv, int64_t rows, int sms, int max_threads, int short_T, RowPlan* q)
 {
-    q->vpt = nv <= 64 ? 2 : 4;
-    const int64_t T = ((nv + q->vpt - 1) / q->vpt + 31) / 32 * 32;
-    if (T > 512) return false;
-    q->T = static_cast<int>(T);
-    q->G = max_threads / q->T > 1 ? max_threads / q->T : 1;
-    if (q->G > MAX_GROUPS) q->G = MAX_GROUPS;
-    if (q->T > 32 && q->G > 8) q->G = 8;   // one named barrier each
+    const auto plan = [&](int vpt) {
+        const int64_t T = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+        if (T > 512) return false;
+        q->vpt = vpt;
+        q->T = static_cast<int>(T);
+        q->G = max_threads / q->T > 1 ? max_threads / q->T : 1;
+        if (q->G > MAX_GROUPS) q->G = MAX_GROUPS;
+        if (q->T > 32 && q->G > 8) q->G = 8;   // one named barrier each
+        return true;
+    };
+    const int64_t at_once = (rows + sms - 1) / sms;   // rows of a CTA
+    if (plan(2) && q->T <= short_T && at_once <= q->G) {
+        q->G = at_once > 1 ? static_cast<int>(at_once) : 1;
+        return true;
+    }
+    if (!plan(nv <= 64 ? 2 : 4)) return false;
+    if (rows <= sms) q->G = 1;
     return true;
 }
 
