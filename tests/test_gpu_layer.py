@@ -101,7 +101,9 @@ def prod(a, b, K):
 
 # ---------------------------------------------------------------- norm
 NORM_SHAPES = [(1, 1), (1, 8), (3, 7), (2, 33), (5, 250), (4, 256), (7, 1000), (3, 1024), (2, 4096), (2, 4109), (3, 5120),
-               (2, 8192), (1, 8199), (2, 16384), (1, 40000), (700, 264)]
+               (2, 8192), (1, 8199), (2, 16384), (1, 40000), (700, 264),
+               # all rows at once, several in a CTA
+               (153, 4096), (305, 1116), (423, 1115), (200, 2441)]
 
 
 def norm64(x, r, g, b, kind, eps):
@@ -209,7 +211,7 @@ LIN_SHAPES = [  # rows, n_out, n_in
     (300, 344, 1024), (257, 513, 328), (1, 4096, 4096), (5, 2048, 4104), (1000, 40, 40),
     # more 128 x 128 tiles than SMs: pairs of CTAs, several tiles each, ragged ends, one contraction block, one column block
     (1700, 1800, 1504), (1701, 1801, 1496), (2049, 2312, 520), (5000, 600, 8), (20001, 8, 64), (24, 136, 2048),
-    (32, 1000, 2056)]
+    (32, 1000, 2056), (70, 1000, 4104), (500, 1100, 2056)]
 ACTS = ["none", "relu", "silu", "gelu_tanh", "gelu_erf"]
 
 
@@ -290,7 +292,7 @@ def test_linear_bwd(dev, R, N, K, dt, gdt):
 FFN_SHAPES = [  # rows, hidden, width
     (1, 8, 8), (1, 520, 65), (2, 72, 64), (6, 5120, 3456), (9, 64, 136), (16, 256, 264), (17, 1000, 72), (40, 136, 200),
     (128, 64, 64), (129, 328, 130), (300, 1024, 344), (1, 4096, 1024), (24, 512, 1000), (32, 2056, 72),
-    (1300, 1904, 904), (1281, 2000, 901), (10001, 64, 72)]
+    (1300, 1904, 904), (1281, 2000, 901), (10001, 64, 72), (12, 4104, 200), (24, 1032, 264), (70, 2056, 1000)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
